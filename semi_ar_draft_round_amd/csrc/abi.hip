@@ -5,6 +5,7 @@
 
 #include <atomic>
 
+#include "cache.hpp"
 #include "common.hpp"
 #include "rnn_head.hpp"
 #include "sample_common.hpp"
@@ -79,6 +80,9 @@ bool draft_shape_ok(int R, int gamma, int V) {
 std::atomic<int> g_device_kind[64];
 std::atomic<int> g_device_cus[64];
 
+}  // namespace
+
+// DSPARK_OK if the current device is a gfx950 GPU (also used by cache_abi.hip).
 dspark_status check_device() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return DSPARK_EDEVICE;
@@ -93,8 +97,6 @@ dspark_status check_device() {
   }
   return kind == 1 ? DSPARK_OK : DSPARK_EDEVICE;
 }
-
-}  // namespace
 
 // Compute units of the current device (valid after a successful check_device).
 int compute_units() {
@@ -111,6 +113,7 @@ using namespace dspark;
 extern "C" {
 
 const char* dspark_status_string(dspark_status s) {
+  if (static_cast<int>(s) == DSPARK_ENOPAGES) return "no free pages for a request (device status)";
   switch (s) {
     case DSPARK_OK: return "success";
     case DSPARK_EINVAL: return "invalid size or pointer argument";

@@ -214,6 +214,21 @@ def run_round_four_calls(d: DeviceRound):
     verify(d)
 
 
+def run_round_cached(d: DeviceRound, cache, forward):
+    """The round with the target's paged cache (cache.PagedCache) in it:
+    pages for the admitted rows after the schedule, forward(d, cache, ell) as
+    the target's pass over them (cache.append and cache.attend per layer; its
+    logits go to d.target), and after the verification the accepted rows
+    kept.  A request that got no pages (ell -1) keeps its cache as it was;
+    its n_acc and next_tok are then of no use."""
+    sample_conf(d)
+    schedule(d)
+    ell = cache.reserve(d.ell, d.gamma)
+    forward(d, cache, ell)
+    verify(d)
+    cache.commit(d.n_acc)
+
+
 def outputs_to_host(d: DeviceRound) -> dict:
     torch.cuda.synchronize()
     return dict(x=d.x.cpu().numpy(), lse=d.lse.cpu().numpy(), logit=d.logit.cpu().numpy(),
