@@ -32,7 +32,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
-  int R, gamma, Hq, Hkv, P, n_pages, max_pages;
+  int R, gamma, Hq, Hkv, G, P, n_pages, max_pages;
   int blocks;              // row blocks a request can have
   int min_units;           // the least units worth a work group
   int slot_tiles;          // row tiles of a workspace slot
@@ -73,54 +73,53 @@ __device__ __forceinline__ bf16x8 as_bf16(u32x4 x) {
   return c.b;
 }
 
-// The tiles that a block of query tokens [i0, i1] of a request can see: tiles
-// 0 .. head - 1, then `first` .. last; count in all.
-struct Span {
-  int head, first, count;
-};
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int64_t len, int i0, int i1) {
-  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.P;
-  int64_t end = len + i1 + 1;
-  if (end > cap) end = cap;
-  const int tiles = static_cast<int>((end + kTile - 1) / kTile);
-  Span s{0, 0, tiles};
-  if (a.window > 0) {
-    const int64_t low = len + i0 - a.window + 1;
-    const int first = low > 0 ? static_cast<int>(low / kTile) : 0;
-    const int64_t sk = a.sinks < end ? a.sinks : end;
-    s.head = static_cast<int>((sk + kTile - 1) / kTile);
-    if (s.head > first) s.head = first;
-    s.first = first;
-    s.count = s.head + (tiles > first ? tiles - first : 0);
-  }
-  if (s.count == 0) {  // nothing to see: one tile, all of it masked, writes the empty result
-    s.first = tiles - 1;
-    s.count = 1;
-  }
-  return s;
+// A (quotient of) counts below 2^52, by a double division and its correction:
+// shorter code than the 64-bit integer division.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  int64_t q = static_cast<int64_t>(static_cast<double>(x) / static_cast<double>(y));
+  const int64_t r = x - q * y;
+  if (r < 0) --q;
+  if (r >= y) ++q;
+  return q;
 }
 
-// A request's row block: its query rows m0 .. m0 + rows - 1.
+// A request's row block: its query rows m0 .. m0 + rows - 1, and the tiles
+// any of them can see: tiles 0 .. head - 1, then first .., count in all.
+// Tokens past the table's reach do not exist, so positions fit 32 bits.
 struct Block {
-  int n, m0, rows;
-  int64_t len;
-  Span span;
+  int m0, rows;
+  int len;               // the first new token, at most kFar
+  int head, first, count;
+  int shift;             // log2 of the waves along the rows (1, 2, 4, 8)
 };
+constexpr int kFar = 1 << 29;  // past every table (2^20 pages of 128 tokens)
+
 __device__ __forceinline__ Block block_of(const AttnArgs& a, int entry, int rows_max) {
   const int r = entry / a.blocks, c = entry % a.blocks;
-  const int G = a.Hq / a.Hkv;
-  Block b;
-  b.n = rows_of(a.ell[r], a.gamma);
-  b.len = a.len[r];
-  b.m0 = c * rows_max;
-  const int M = b.n * G;
-  b.rows = min(rows_max, M - b.m0);
-  if (b.rows <= 0 || b.len < 0) {
+  const int n = rows_of(a.ell[r], a.gamma);
+  const int len = a.len[r];
+  Block b{c * rows_max, 0, min(len, kFar), 0, 0, 0, 0};
+  b.rows = min(rows_max, n * a.G - b.m0);
+  if (b.rows <= 0 || len < 0) {
     b.rows = 0;
-    b.span = Span{0, 0, 0};
     return b;
   }
-  b.span = span_of(a, b.len, b.m0 / G, (b.m0 + b.rows - 1) / G);
+  const int qt = (b.rows + kTile - 1) / kTile;
+  b.shift = qt == 1 ? 0 : 32 - __clz(qt - 1);
+  const int cap = a.max_pages * a.P;
+  const int end = min(b.len + (b.m0 + b.rows - 1) / a.G + 1, cap);
+  const int tiles = (end + kTile - 1) / kTile;
+  b.count = tiles;
+  if (a.window > 0) {
+    const int low = b.len + b.m0 / a.G + 1 - a.window;
+    b.first = low > 0 ? low / kTile : 0;
+    b.head = min((min(a.sinks, end) + kTile - 1) / kTile, b.first);
+    b.count = b.head + max(tiles - b.first, 0);
+  }
+  if (b.count == 0) {  // nothing to see: one tile, all of it masked, writes the empty result
+    b.first = tiles - 1;
+    b.count = 1;
+  }
   return b;
 }
 
@@ -297,312 +296,328 @@ __device__ __forceinline__ void add_non_finite(f32x16 (&o)[D / 32], const float 
   }
 }
 
+// The range of units of work group wg: `share` each, the first `rest` one more.
+struct Deal {
+  int64_t share, rest;
+  __device__ __forceinline__ int64_t begin(int64_t wg) const { return share * wg + (wg < rest ? wg : rest); }
+  __device__ __forceinline__ int owner(int64_t unit) const {
+    const int64_t big = rest * (share + 1);
+    return static_cast<int>(unit < big ? quotient(unit, share + 1) : rest + quotient(unit - big, share));
+  }
+};
+
 template <int FMT, int D>
 __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(AttnArgs a) {
   typedef PageLayout<FMT, D> L;
   constexpr int W = Shape<D>::kWaves, T = W * 64, NB = D / 32, KS = D / 16;
+  constexpr float kSlack = 8.f;  // a weight may reach 2^8 before the sums are rescaled
   __shared__ f32x4 lds_o[W / 2][NB * 4][64];
   __shared__ float2 lds_ml[W / 2][64];
   __shared__ int64_t lds_scan[W];
   __shared__ int64_t lds_base;
   __shared__ int lds_entry;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, col = lane & 31;
-  const int rows_max = W * kTile;
-  const int G = a.Hq / a.Hkv;
+  constexpr int rows_max = W * kTile;
+  const int wg = blockIdx.x;
 
-  // Units before every entry (request, row block): runs of entries per thread, then a scan.
+  // Units before every entry (request, row block): runs of entries per
+  // thread and a scan.  A tile counts once per wave along the rows, the time
+  // it takes.  The second pass looks up where this work group's run begins.
   const int entries = a.R * a.blocks;
   const int per = ceil_div(entries, T);
   const int e0 = min(entries, static_cast<int>(threadIdx.x) * per), e1 = min(entries, e0 + per);
-  int64_t mine = 0;
-  for (int e = e0; e < e1; ++e) {
-    const Block b = block_of(a, e, rows_max);
-    if (b.rows > 0) mine += static_cast<int64_t>(b.span.count) * a.Hkv;
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t t = __shfl_up(incl, o);
-    if (lane >= o) incl += t;
-  }
-  if (lane == 63) lds_scan[wave] = incl;
-  __syncthreads();
-  int64_t before = 0, N = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const int64_t s = lds_scan[w];
-    if (w < wave) before += s;
-    N += s;
-  }
-  const int64_t units_wg = N / a.min_units;
-  const int nb = units_wg < 1 ? 1 : units_wg < gridDim.x ? static_cast<int>(units_wg) : static_cast<int>(gridDim.x);
-  const int wg = blockIdx.x;
-  Desc left{0, 0, 0, 0};
-  if (wg < nb && N > 0) {
-    const int64_t u0 = N * wg / nb, u1 = N * (wg + 1) / nb;
-    int64_t at = before + incl - mine;
-    if (u0 >= at && u0 < at + mine) {
-      int e = e0;
-      for (; e < e1; ++e) {
-        const Block b = block_of(a, e, rows_max);
-        const int64_t n = b.rows > 0 ? static_cast<int64_t>(b.span.count) * a.Hkv : 0;
-        if (u0 < at + n) break;
-        at += n;
+  Deal deal{0, 0};
+  int64_t at = 0, u0 = 0, u1 = 0;
+  int nb = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const Block b = block_of(a, e, rows_max);
+      const int64_t n = (static_cast<int64_t>(b.count) << b.shift) * a.Hkv;
+      if (pass == 1 && u0 >= at + sum && u0 < at + sum + n) {
+        lds_entry = e;
+        lds_base = at + sum;
       }
-      lds_entry = e;
-      lds_base = at;
+      sum += n;
     }
-    __syncthreads();
-    int entry = lds_entry;
-    int64_t base = lds_base;
-
-    for (int64_t u = u0; u < u1;) {
-      const Block b = block_of(a, entry, rows_max);
-      const int64_t total = b.rows > 0 ? static_cast<int64_t>(b.span.count) * a.Hkv : 0;
-      if (u >= base + total) {
-        base += total;
-        ++entry;
-        continue;
+    if (pass == 0) {
+      int64_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int64_t t = __shfl_up(incl, o);
+        if (lane >= o) incl += t;
       }
-      const int r = entry / a.blocks;
-      const int hk = static_cast<int>((u - base) / b.span.count);
-      const int64_t seg = base + static_cast<int64_t>(hk) * b.span.count;
-      const int t0 = static_cast<int>(u - seg);
-      const int t1 = u1 - seg < b.span.count ? static_cast<int>(u1 - seg) : b.span.count;
-      const int qt = ceil_div(b.rows, kTile);
-      const int WT = qt == 1 ? W : qt == 2 ? W / 2 : qt <= 4 ? W / 4 : 1;  // waves along the tokens
-      const int wq = wave % qt, wt = wave / qt;
-      const bool active = wt < WT;
-
-      // this lane's query row
-      const int row = min(wq * kTile + col, b.rows - 1);
-      const int i = (b.m0 + row) / G, g = (b.m0 + row) % G;
-      const int64_t first_row =
-          a.row0 ? static_cast<int64_t>(a.row0[r]) : static_cast<int64_t>(r) * (a.gamma + 1);
-      const int64_t out_at = ((first_row + i) * a.Hq + hk * G + g);
-      const int64_t pos = b.len + i;
-      const int64_t low = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-      // the wave's first and last rows
-      const int row_a = min(wq * kTile, b.rows - 1), row_b = min(wq * kTile + kTile, b.rows) - 1;
-      const int64_t pos_a = b.len + (b.m0 + row_a) / G, pos_b = b.len + (b.m0 + row_b) / G;
-      const int64_t low_a = a.window > 0 && pos_a - a.window + 1 > 0 ? pos_a - a.window + 1 : 0;
-      const int64_t low_b = a.window > 0 && pos_b - a.window + 1 > 0 ? pos_b - a.window + 1 : 0;
-
-      Acc<D> acc;
-      acc.m = neg_inf();
-      acc.l = 0.f;
+      if (lane == 63) lds_scan[wave] = incl;
+      __syncthreads();
+      int64_t before = 0, N = 0;
 #pragma unroll
-      for (int x = 0; x < NB; ++x) acc.o[x] = f32x16{0.f};
+      for (int w = 0; w < W; ++w) {
+        const int64_t s = lds_scan[w];
+        if (w < wave) before += s;
+        N += s;
+      }
+      at = before + incl - sum;
+      const int64_t useful = N / a.min_units;  // a power of two
+      nb = useful < 1 ? 1 : useful < gridDim.x ? static_cast<int>(useful) : static_cast<int>(gridDim.x);
+      deal.share = quotient(N, nb);
+      deal.rest = N - deal.share * nb;
+      u0 = deal.begin(wg);
+      u1 = wg < nb ? deal.begin(wg + 1) : u0;
+    }
+  }
+  __syncthreads();
+  Desc left{0, 0, 0, 0};
+  int entry = u0 < u1 ? __builtin_amdgcn_readfirstlane(lds_entry) : 0;
+  int64_t base = u0 < u1 ? lds_base : 0;
 
-      const int steps = active && t0 + wt < t1 ? (t1 - t0 - wt + WT - 1) / WT : 0;
-      if (steps > 0) {
-        u32x4 q[KS];
+#pragma unroll 1
+  for (int64_t u = u0; u < u1;) {
+    const Block b = block_of(a, entry, rows_max);
+    const int64_t per_head = static_cast<int64_t>(b.count) << b.shift;
+    if (u >= base + per_head * a.Hkv) {
+      base += per_head * a.Hkv;
+      ++entry;
+      continue;
+    }
+    const int r = entry / a.blocks;
+    const int hk = static_cast<int>(quotient(u - base, per_head));
+    const int64_t seg = base + hk * per_head, seg_end = seg + per_head;
+    // the tiles whose first unit is in this run
+    const int weight = 1 << b.shift;
+    const int t0 = static_cast<int>((u - seg + weight - 1) >> b.shift);
+    const int t1 = u1 < seg_end ? static_cast<int>((u1 - seg + weight - 1) >> b.shift) : b.count;
+    u = seg_end;
+    if (t0 >= t1) continue;
+    const int qt = ceil_div(b.rows, kTile);
+    const int WT = W >> b.shift;  // waves along the tokens
+    const int wq = wave % qt, wt = wave / qt;
+    const bool active = wt < WT;
+
+    // this lane's query row
+    const int row = min(wq * kTile + col, b.rows - 1);
+    const int i = (b.m0 + row) / a.G, g = (b.m0 + row) - i * a.G;
+    const int64_t first_row = a.row0 ? static_cast<int64_t>(a.row0[r]) : static_cast<int64_t>(r) * (a.gamma + 1);
+    const int64_t out_at = (first_row + i) * a.Hq + hk * a.G + g;
+    const int pos = b.len + i;
+    const int low = a.window > 0 ? pos - a.window + 1 : 0;  // window < 2^31 and pos < 2^30: no overflow
+    // the wave's first and last rows
+    const int pos_a = b.len + (b.m0 + min(wq * kTile, b.rows - 1)) / a.G;
+    const int pos_b = b.len + (b.m0 + min(wq * kTile + kTile, b.rows) - 1) / a.G;
+    const int low_a = a.window > 0 ? pos_a - a.window + 1 : 0;
+    const int low_b = a.window > 0 ? pos_b - a.window + 1 : 0;
+
+    Acc<D> acc;
+    acc.m = neg_inf();
+    acc.l = 0.f;
 #pragma unroll
-        for (int x = 0; x < KS; ++x) {
-          q[x] = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
+    for (int x = 0; x < NB; ++x) acc.o[x] = f32x16{0.f};
+
+    const int steps = active && t0 + wt < t1 ? (t1 - t0 - wt + WT - 1) >> (__ffs(WT) - 1) : 0;
+    if (steps > 0) {
+      u32x4 q[KS];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) q[x][y] = (q[x][y] & a.q_keep) ^ a.q_flip;
-        }
-        const int64_t head_off = hk * L::head_bytes(a.P);
-        const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
-        const int lp = 31 - __clz(a.P);
-        // page ids of the wave's next 64 tiles, one tile a lane (two pages a tile when P is 16)
-        int id0_v = -1, id1_v = -1;
-        auto tile_at = [&](int k) {
-          const int t = t0 + wt + k * WT;
-          return t < b.span.head ? t : t - b.span.head + b.span.first;
-        };
-        auto fetch_ids = [&](int k0) {
-          const int64_t tok = static_cast<int64_t>(tile_at(k0 + lane)) * kTile;
-          const int64_t s0 = tok >> lp, s1 = (tok + 16) >> lp;
-          const bool in = k0 + lane < steps;
-          id0_v = in && s0 < a.max_pages ? page_or_none(table[s0], a.n_pages) : -1;
-          id1_v = in && s1 < a.max_pages ? page_or_none(table[s1], a.n_pages) : -1;
-        };
-        KTile<FMT, D> kt;
-        VTile<FMT, D> vt;
-        // pages of the tile in flight; a missing one is read as page 0 and masked
-        int id0 = 0, id1 = 0;
-        int64_t tok = 0;
-        const char *head0 = nullptr, *head1 = nullptr;
-        int in0 = 0, in1 = 0;
-        auto aim = [&](int k) {
-          if ((k & 63) == 0) fetch_ids(k);
-          id0 = __builtin_amdgcn_readlane(id0_v, k & 63);
-          id1 = __builtin_amdgcn_readlane(id1_v, k & 63);
-          tok = static_cast<int64_t>(tile_at(k)) * kTile;
-          head0 = a.pool + max(id0, 0) * a.page_bytes + head_off;
-          head1 = a.pool + max(id1, 0) * a.page_bytes + head_off;
-          in0 = static_cast<int>(tok & (a.P - 1));
-          in1 = static_cast<int>((tok + 16) & (a.P - 1));
-        };
-        auto load_k = [&]() {
-          kt.load(col < 16 ? head0 : head1, a.P, (col < 16 ? in0 : in1) + token_of_slot(col & 15), h);
-        };
-        aim(0);
+      for (int x = 0; x < KS; ++x) {
+        q[x] = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) q[x][y] = (q[x][y] & a.q_keep) ^ a.q_flip;
+      }
+      const char* pool = a.pool + hk * L::head_bytes(a.P);
+      const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
+      const int lp = 31 - __clz(a.P);
+      // page ids of the wave's next 64 tiles, a tile a lane (two pages a tile
+      // when P is 16), and which of those tiles need no mask
+      int id0_v = -1, id1_v = -1;
+      unsigned long long clear_v = 0;
+      auto tile_at = [&](int k) {
+        const int t = t0 + wt + k * WT;
+        return t < b.head ? t : t - b.head + b.first;
+      };
+      auto fetch_ids = [&](int k0) {
+        const int k = min(k0 + lane, steps - 1), tok = tile_at(k) * kTile;
+        const int s0 = tok >> lp, s1 = (tok + 16) >> lp;
+        id0_v = s0 < a.max_pages ? page_or_none(table[s0], a.n_pages) : -1;
+        id1_v = s1 < a.max_pages ? page_or_none(table[s1], a.n_pages) : -1;
+        clear_v = __ballot(id0_v >= 0 && id1_v >= 0 && tok + kTile - 1 <= pos_a &&
+                           (tok >= low_b || tok + kTile <= a.sinks));
+      };
+      KTile<FMT, D> kt;
+      VTile<FMT, D> vt;
+      // the tile in flight; a missing page is read as page 0 and masked
+      int id0 = 0, id1 = 0, tok = 0;
+      const char *head0 = nullptr, *head1 = nullptr;
+      auto aim = [&](int k) {
+        id0 = __builtin_amdgcn_readlane(id0_v, k & 63);
+        id1 = __builtin_amdgcn_readlane(id1_v, k & 63);
+        tok = tile_at(k) * kTile;
+        head0 = pool + max(id0, 0) * a.page_bytes;
+        head1 = pool + max(id1, 0) * a.page_bytes;
+      };
+      auto load_k = [&]() {
+        kt.load(col < 16 ? head0 : head1, a.P, ((tok + (col & 16)) & (a.P - 1)) + token_of_slot(col & 15), h);
+      };
+      auto load_v = [&]() {
+        vt.load(0, head0, a.P, tok & (a.P - 1), col, h);
+        vt.load(1, head1, a.P, (tok + 16) & (a.P - 1), col, h);
+      };
+      fetch_ids(0);
+      aim(0);
+      load_k();
+      load_v();
+#pragma unroll 1
+      for (int k = 0; k < steps; ++k) {
+        f32x16 s = kt.scores(q, h);
+        const bool clear = (clear_v >> (k & 63)) & 1u;
+        const int c0 = id0, c1 = id1, ct = tok;
+        const char *ch0 = head0, *ch1 = head1;
+        // the next tile's keys (after the last tile: its own again, unused)
+        const int next = min(k + 1, steps - 1);
+        if ((k & 63) == 63) fetch_ids(next);
+        aim(next);
         load_k();
-        vt.load(0, head0, a.P, in0, col, h);
-        vt.load(1, head1, a.P, in1, col, h);
-        for (int k = 0; k < steps; ++k) {
-          f32x16 s = kt.scores(q, h);
-          const int c0 = id0, c1 = id1, ci0 = in0, ci1 = in1;
-          const int64_t ct = tok;
-          const char *ch0 = head0, *ch1 = head1;
-          const bool more = k + 1 < steps;
-          if (more) {
-            aim(k + 1);
-            load_k();
-          }
-          const bool clear = c0 >= 0 && c1 >= 0 && ct + kTile - 1 <= pos_a && (ct >= low_b || ct + kTile <= a.sinks);
-          uint32_t visible = 0xFFFFu;
-          if (!clear) {
-            visible = 0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int64_t t = ct + 16 * (j / 8) + 8 * h + j % 8;
-              const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
-              s[j] = see ? s[j] : neg_inf();
-              visible |= static_cast<uint32_t>(see) << j;
-            }
-          }
-          float top = s[0];
-#pragma unroll
-          for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
-          top = fmaxf(top, xor32(top));
-          const float m = fmaxf(acc.m, top * a.scale_log2);
-          const float ref = m == neg_inf() ? 0.f : m;
-          float p[16], sum = 0.f;
+        uint32_t visible = 0xFFFFu;
+        if (!clear) {
+          visible = 0;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, -ref));
-            sum += p[j];
-          }
-          if (__any(m != acc.m)) {
-            const float keep = __builtin_amdgcn_exp2f(acc.m - ref);
-            acc.l *= keep;
-            acc.m = m;
-#pragma unroll
-            for (int x = 0; x < NB; ++x)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) acc.o[x][j] *= keep;
-          }
-          acc.l += sum;
-          u32x4 pk[2];
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float x = vt.weight(j, p[j]), y = vt.weight(j + 1, p[j + 1]);
-            if (FMT == DSPARK_CACHE_FP4 && !clear) {  // a hidden token's scale may be anything
-              x = (visible >> j) & 1u ? x : 0.f;
-              y = (visible >> (j + 1)) & 1u ? y : 0.f;
-            }
-            pk[j / 8][(j % 8) / 2] = bf16_pair(x, y);
-          }
-          bool odd = false;
-          if (FMT == DSPARK_CACHE_BF16 && !clear) {
-            // tokens that no row of the wave sees become zeros; of the others, values that are not finite too
-            if constexpr (FMT == DSPARK_CACHE_BF16) {
-#pragma unroll
-              for (int s2 = 0; s2 < 2; ++s2) {
-                u32x4 keep{0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int64_t t = ct + 16 * s2 + 8 * h + e;
-                  const bool see = (s2 ? c1 : c0) >= 0 && t <= pos_b && (t >= low_a || t < a.sinks);
-                  keep[e / 2] |= see ? 0xFFFFu << (16 * (e & 1)) : 0u;
-                }
-#pragma unroll
-                for (int x = 0; x < NB; ++x)
-#pragma unroll
-                  for (int w = 0; w < 4; ++w) {
-                    uint32_t v = vt.x[s2][x][w] & keep[w];
-                    if ((v & 0x7F80u) == 0x7F80u) odd = true, v &= 0xFFFF0000u;
-                    if ((v & 0x7F800000u) == 0x7F800000u) odd = true, v &= 0x0000FFFFu;
-                    vt.x[s2][x][w] = v;
-                  }
-              }
-            }
-          }
-#pragma unroll
-          for (int s2 = 0; s2 < 2; ++s2)
-#pragma unroll
-            for (int x = 0; x < NB; ++x)
-              acc.o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vt.operand(s2, x)), as_bf16(pk[s2]), acc.o[x],
-                                                                 0, 0, 0);
-          if constexpr (FMT == DSPARK_CACHE_BF16)
-            if (__any(odd)) add_non_finite<D>(acc.o, p, visible, ch0, ch1, a.P, ci0, ci1, lane);
-          if (more) {
-            vt.load(0, head0, a.P, in0, col, h);
-            vt.load(1, head1, a.P, in1, col, h);
+            const int t = ct + 16 * (j / 8) + 8 * h + j % 8;
+            const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
+            s[j] = see ? s[j] : neg_inf();
+            visible |= static_cast<uint32_t>(see) << j;
           }
         }
-      }
-
-      // join the waves along the tokens, halving
-      for (int step = WT / 2; step >= 1; step >>= 1) {
-        __syncthreads();
-        if (active && wt >= step && wt < 2 * step) {
-          const int slot = (wt - step) * qt + wq;
-          lds_ml[slot][lane] = make_float2(acc.m, acc.l);
+        float top = s[0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
+        top = fmaxf(top, xor32(top)) * a.scale_log2;
+        // weights are relative to acc.m, which follows the maximum once that is 2^8 ahead
+        if (__any(top > acc.m + kSlack)) {
+          const float m = fmaxf(acc.m, top);
+          const float keep = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(acc.m - m);
+          acc.l *= keep;
+          acc.m = m;
 #pragma unroll
           for (int x = 0; x < NB; ++x)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              lds_o[slot][x * 4 + j][lane] =
-                  f32x4{acc.o[x][4 * j], acc.o[x][4 * j + 1], acc.o[x][4 * j + 2], acc.o[x][4 * j + 3]};
+            for (int j = 0; j < 16; ++j) acc.o[x][j] *= keep;
         }
-        __syncthreads();
-        if (active && wt < step) {
-          const int slot = wt * qt + wq;
-          const float2 ml = lds_ml[slot][lane];
-          float sa, sb;
-          join<D>(acc, ml.x, ml.y, &sa, &sb);
+        const float ref = acc.m == neg_inf() ? 0.f : acc.m;
+        float p[16], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, -ref));
+          sum += p[j];
+        }
+        acc.l += sum;
+        u32x4 pk[2];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) pk[j / 8][(j % 8) / 2] = bf16_pair(vt.weight(j, p[j]), vt.weight(j + 1, p[j + 1]));
+        bool odd = false;
+        if (!clear) {
+          if constexpr (FMT == DSPARK_CACHE_FP4) {  // a hidden token's scale may be anything
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+              pk[j / 8][(j % 8) / 2] &=
+                  ((visible >> j) & 1u ? 0xFFFFu : 0u) | ((visible >> (j + 1)) & 1u ? 0xFFFF0000u : 0u);
+          } else {
+            // tokens that no row of the wave sees become zeros; of the others, values that are not finite too
+#pragma unroll
+            for (int s2 = 0; s2 < 2; ++s2) {
+              u32x4 keep{0u, 0u, 0u, 0u};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int t = ct + 16 * s2 + 8 * h + e;
+                const bool see = (s2 ? c1 : c0) >= 0 && t <= pos_b && (t >= low_a || t < a.sinks);
+                keep[e / 2] |= see ? 0xFFFFu << (16 * (e & 1)) : 0u;
+              }
+#pragma unroll
+              for (int x = 0; x < NB; ++x)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  uint32_t v = vt.x[s2][x][w] & keep[w];
+                  if ((v & 0x7F80u) == 0x7F80u) odd = true, v &= 0xFFFF0000u;
+                  if ((v & 0x7F800000u) == 0x7F800000u) odd = true, v &= 0x0000FFFFu;
+                  vt.x[s2][x][w] = v;
+                }
+            }
+          }
+        }
+#pragma unroll
+        for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+          for (int x = 0; x < NB; ++x)
+            acc.o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vt.operand(s2, x)), as_bf16(pk[s2]), acc.o[x], 0,
+                                                               0, 0);
+        if constexpr (FMT == DSPARK_CACHE_BF16)
+          if (__any(odd))
+            add_non_finite<D>(acc.o, p, visible, ch0, ch1, a.P, ct & (a.P - 1), (ct + 16) & (a.P - 1), lane);
+        load_v();
+      }
+    }
+
+    // join the waves along the tokens, halving
+#pragma unroll 1
+    for (int step = WT / 2; step >= 1; step >>= 1) {
+      if (active && wt >= step && wt < 2 * step) {
+        const int slot = (wt - step) * qt + wq;
+        lds_ml[slot][lane] = make_float2(acc.m, acc.l);
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            lds_o[slot][x * 4 + j][lane] =
+                f32x4{acc.o[x][4 * j], acc.o[x][4 * j + 1], acc.o[x][4 * j + 2], acc.o[x][4 * j + 3]};
+      }
+      __syncthreads();
+      if (active && wt < step) {
+        const int slot = wt * qt + wq;
+        const float2 ml = lds_ml[slot][lane];
+        float sa, sb;
+        join<D>(acc, ml.x, ml.y, &sa, &sb);
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 y = lds_o[slot][x * 4 + j][lane];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) acc.o[x][4 * j + z] = acc.o[x][4 * j + z] * sa + y[z] * sb;
+          }
+      }
+      __syncthreads();
+    }
+
+    const bool opens = t0 == 0, closes = t1 == b.count;
+    if (active && wt == 0) {
+      const float l = acc.l + xor32(acc.l);
+      if (opens && closes) {
+        if (wq * kTile + col < b.rows) {
+          const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
           for (int x = 0; x < NB; ++x)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const f32x4 y = lds_o[slot][x * 4 + j][lane];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) acc.o[x][4 * j + z] = acc.o[x][4 * j + z] * sa + y[z] * sb;
+              const u32x2 w{bf16_pair(acc.o[x][4 * j] * inv, acc.o[x][4 * j + 1] * inv),
+                            bf16_pair(acc.o[x][4 * j + 2] * inv, acc.o[x][4 * j + 3] * inv)};
+              *reinterpret_cast<u32x2*>(a.out + out_at * D + x * 32 + 8 * j + 4 * h) = w;
             }
+          if (a.lse && h == 0) a.lse[out_at] = l != 0.f ? (acc.m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
         }
+      } else {
+        const int64_t slot = (static_cast<int64_t>(wg) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
+        if (h == 0) a.ml[slot * kTile + col] = make_float2(acc.m, l);
+        f32x4* dst = reinterpret_cast<f32x4*>(a.part) + slot * (NB * 4 * 64);
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[(x * 4 + j) * 64 + lane] =
+                f32x4{acc.o[x][4 * j], acc.o[x][4 * j + 1], acc.o[x][4 * j + 2], acc.o[x][4 * j + 3]};
       }
-      __syncthreads();
-
-      const bool opens = t0 == 0, closes = t1 == b.span.count;
-      if (active && wt == 0) {
-        const float l = acc.l + xor32(acc.l);
-        if (opens && closes) {
-          if (wq * kTile + col < b.rows) {
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-            for (int x = 0; x < NB; ++x)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const u32x2 w{bf16_pair(acc.o[x][4 * j] * inv, acc.o[x][4 * j + 1] * inv),
-                              bf16_pair(acc.o[x][4 * j + 2] * inv, acc.o[x][4 * j + 3] * inv)};
-                *reinterpret_cast<u32x2*>(a.out + out_at * D + x * 32 + 8 * j + 4 * h) = w;
-              }
-            if (a.lse && h == 0) a.lse[out_at] = l != 0.f ? (acc.m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
-          }
-        } else {
-          const int64_t slot = (static_cast<int64_t>(wg) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
-          if (h == 0) a.ml[slot * kTile + col] = make_float2(acc.m, l);
-          f32x4* dst = reinterpret_cast<f32x4*>(a.part) + slot * (NB * 4 * 64);
-#pragma unroll
-          for (int x = 0; x < NB; ++x)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              dst[(x * 4 + j) * 64 + lane] =
-                  f32x4{acc.o[x][4 * j], acc.o[x][4 * j + 1], acc.o[x][4 * j + 2], acc.o[x][4 * j + 3]};
-        }
-      }
-      if (opens && !closes) {
-        const int64_t end = seg + b.span.count;  // the work group that holds unit end - 1 has the last part
-        left = Desc{static_cast<int>((end * nb - 1) / N) - wg + 1, r, entry % a.blocks, hk};
-      }
-      u = seg + t1;
     }
+    if (opens && !closes)  // the work group that holds the last tile's first unit has the last part
+      left = Desc{deal.owner(seg_end - weight) - wg + 1, r, entry - r * a.blocks, hk};
   }
   if (threadIdx.x == 0) reinterpret_cast<Desc*>(a.desc)[wg] = left;
 }
@@ -633,7 +648,7 @@ __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
 #pragma unroll
     for (int z = 0; z < 4; ++z) o[z] = o[z] * sa + y[z] * sb;
   }
-  const int G = a.Hq / a.Hkv;
+  const int G = a.G;
   const int i = (b.m0 + row) / G, g = (b.m0 + row) % G;
   const int64_t first_row = a.row0 ? static_cast<int64_t>(a.row0[d.r]) : static_cast<int64_t>(d.r) * (a.gamma + 1);
   const int64_t out_at = (first_row + i) * a.Hq + d.head * G + g;
@@ -660,11 +675,11 @@ int slot_tiles_of(int gamma, int Hq, int Hkv, int D) {
 template <int FMT, int D>
 hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
   constexpr int W = Shape<D>::kWaves, NB = D / 32;
-  const int G = a.Hq / a.Hkv;
+  const int G = a.G = a.Hq / a.Hkv;
   a.page_bytes = a.Hkv * PageLayout<FMT, D>::head_bytes(a.P);
   a.blocks = ceil_div(static_cast<int64_t>(a.gamma + 1) * G, W * kTile);
   a.slot_tiles = slot_tiles_of(a.gamma, a.Hq, a.Hkv, D);
-  a.min_units = W;
+  a.min_units = W;  // a power of two, and no less than a tile's weight
   const int grid = grid_of();
   char* p = static_cast<char*>(ws);
   a.desc = reinterpret_cast<int32_t*>(p);
