@@ -10,6 +10,7 @@ import fails, and a non-zero status raises DSparkError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -554,68 +555,82 @@ def dspark_sts_fit(z, n_acc, grid, n_bins=15, ws=None):
 
 # ---------------------------------------------------------------- the paged cache
 
+@functools.lru_cache(maxsize=None)   # a function of small integers
 def dspark_cache_page_bytes(fmt: int, heads_kv: int, dim: int, page: int) -> int:
     return int(load_library().dspark_cache_page_bytes(fmt, heads_kv, dim, page))
 
 
+@functools.lru_cache(maxsize=4096)
 def dspark_cache_workspace_size(kind: int, R: int, gamma: int, a: int, b: int, c: int = 0) -> int:
     return int(load_library().dspark_cache_workspace_size(kind, R, gamma, a, b, c))
 
 
-def _on_current(dev):
-    """Cache calls run on the current device's current stream: tensors of
-    another device are refused."""
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, not on the current GPU")
+def _raw_stream(dev: int) -> int:
+    """The current stream of device `dev`, which must be the current device:
+    cache calls run there, and tensors of another device are refused."""
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on device {dev} (-1: the CPU), not on the current GPU")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _need(t, name, shape, dtype, dev: int):
+    """t must be a contiguous tensor of this shape and type on device dev;
+    returns its address."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _check(t, name, shape, (dtype,), torch.device("cuda", dev) if dev >= 0 else torch.device("cpu"))
+    return t.data_ptr()
+
+
+_I32, _BF, _U8 = torch.int32, torch.bfloat16, torch.uint8
 
 
 def _cache_ws(ws, kind, R, gamma, a, b, c, dev):
     """The given workspace, or one of this call's own from torch's allocator
     (so that no two calls or captured graphs share it)."""
     if ws is None:
-        return torch.empty(max(1, dspark_cache_workspace_size(kind, R, gamma, a, b, c)), dtype=torch.uint8, device=dev)
-    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
+        return torch.empty(max(1, dspark_cache_workspace_size(kind, R, gamma, a, b, c)), dtype=_U8,
+                           device=torch.device("cuda", dev))
+    if ws.dtype is not _U8 or not ws.is_contiguous() or ws.get_device() != dev:
         raise ValueError("ws must be a contiguous uint8 tensor on the call's device")
     return ws
 
 
 def _check_rows(t, name, rows, heads, dim, dev):
     """[rows][heads][dim] bf16 whose rows are contiguous; the row stride in elements."""
-    if t.dim() != 3 or tuple(t.shape) != (rows, heads, dim):
+    if t.shape != (rows, heads, dim):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {(rows, heads, dim)}")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF:
         raise ValueError(f"{name}: dtype {t.dtype} is not bfloat16")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: heads of a row must be contiguous")
-    ld = t.stride(0) if rows > 1 else heads * dim
+    ld = s0 if rows > 1 else heads * dim
     if ld < heads * dim or ld % 8 != 0 or t.data_ptr() % 16 != 0:
         raise ValueError(f"{name}: rows must be 16-byte aligned and not overlap")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not where q is")
     return ld
 
 
-def _check_batch(table, length, ell, gamma, row0, rows, dev):
-    R = table.shape[0]
-    i32 = (torch.int32,)
-    _check(table, "table", (R, table.shape[1]), i32, dev)
-    _check(length, "length", (R,), i32, dev)
-    _check(ell, "ell", (R,), i32, dev)
-    if row0 is not None:
-        _check(row0, "row0", (R,), i32, dev)
-    elif rows != R * (gamma + 1):
+def _batch(table, length, ell, gamma, row0, rows, dev):
+    """R, max_pages and the addresses of row0, ell, length and table."""
+    R, max_pages = table.shape
+    if row0 is None and rows != R * (gamma + 1):
         raise ValueError(f"{rows} rows: without row0 there are R * (gamma + 1) = {R * (gamma + 1)}")
-    return R
+    return (R, max_pages, None if row0 is None else _need(row0, "row0", (R,), _I32, dev),
+            _need(ell, "ell", (R,), _I32, dev), _need(length, "length", (R,), _I32, dev),
+            _need(table, "table", (R, max_pages), _I32, dev))
 
 
-def _check_pool(pool, fmt, heads_kv, dim, page, dev):
+def _pool(pool, fmt, heads_kv, dim, page, dev):
+    """The number of pages and the address of one layer's pool."""
     nb = dspark_cache_page_bytes(fmt, heads_kv, dim, page)
     if nb == 0:
         raise ValueError(f"no page format {fmt} with {heads_kv} heads of {dim} and {page} tokens")
     if pool.dim() != 2:
         raise ValueError("pool must be [n_pages][page bytes]")
-    _check(pool, "pool", (pool.shape[0], nb), (torch.uint8,), dev)
-    return pool.shape[0]
+    n_pages = pool.shape[0]
+    return n_pages, _need(pool, "pool", (n_pages, nb), _U8, dev)
 
 
 def dspark_cache_append(q, k, v, pool, table, length, ell, gamma, *, fmt, page, wq=None, wk=None, eps=1e-6, freq=None,
@@ -624,32 +639,31 @@ def dspark_cache_append(q, k, v, pool, table, length, ell, gamma, *, fmt, page, 
     its own and v go into the pages.  q, k and v may be views of one fused
     projection's rows.  freq [rot / 2] float64: radians per position (None: no
     rotation).  pool [n_pages][page bytes] uint8: one layer's pages."""
-    lib = load_library()
-    dev = q.device
+    dev = q.get_device()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [rows][heads][dim]")
     rows, Hq, D = q.shape
     Hkv = k.shape[1]
-    R = _check_batch(table, length, ell, gamma, row0, rows, dev)
+    R, max_pages, p_row0, p_ell, p_len, p_table = _batch(table, length, ell, gamma, row0, rows, dev)
     ldq = _check_rows(q, "q", rows, Hq, D, dev)
     ldk = _check_rows(k, "k", rows, Hkv, D, dev)
     ldv = _check_rows(v, "v", rows, Hkv, D, dev)
-    n_pages = _check_pool(pool, fmt, Hkv, D, page, dev)
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _check(w, name, (D,), (torch.bfloat16,), dev)
-    rot = 0
+    n_pages, p_pool = _pool(pool, fmt, Hkv, D, page, dev)
+    p_wq = None if wq is None else _need(wq, "wq", (D,), _BF, dev)
+    p_wk = None if wk is None else _need(wk, "wk", (D,), _BF, dev)
+    rot, p_freq = 0, None
     if freq is not None:
-        _check(freq, "freq", (freq.numel(),), (torch.float64,), dev)
         rot = 2 * freq.numel()
-    q_out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-    _check(q_out, "q_out", (rows, Hq, D), (torch.bfloat16,), dev)
-    _on_current(dev)
+        p_freq = _need(freq, "freq", (rot // 2,), torch.float64, dev)
+    if q_out is None:
+        q_out = torch.empty((rows, Hq, D), dtype=_BF, device=q.device)
+    p_out = _need(q_out, "q_out", (rows, Hq, D), _BF, dev)
+    stream = _raw_stream(dev)
     if rows == 0:
         return q_out
-    st = lib.dspark_cache_append(fmt, R, gamma, Hq, Hkv, D, page, n_pages, table.shape[1], _ptr(q), ldq, _ptr(k), ldk,
-                                 _ptr(v), ldv, _ptr(wq), _ptr(wk), eps, _ptr(freq), rot, int(adjacent), _ptr(row0),
-                                 _ptr(ell), _ptr(length), _ptr(table), _ptr(q_out), _ptr(pool), _stream())
+    st = load_library().dspark_cache_append(fmt, R, gamma, Hq, Hkv, D, page, n_pages, max_pages, q.data_ptr(), ldq,
+                                            k.data_ptr(), ldk, v.data_ptr(), ldv, p_wq, p_wk, eps, p_freq, rot,
+                                            int(adjacent), p_row0, p_ell, p_len, p_table, p_out, p_pool, stream)
     _raise("dspark_cache_append", st)
     return q_out
 
@@ -660,26 +674,25 @@ def dspark_cache_attention(q, pool, table, length, ell, gamma, *, fmt, page, hea
     rows' attention over the cache with the rows that append has just
     written.  window 0: all tokens up to the row's own; else the last
     `window` of them and the first `sinks`.  scale None: D ** -0.5."""
-    lib = load_library()
-    dev = q.device
+    dev = q.get_device()
     if q.dim() != 3:
         raise ValueError("q must be [rows][heads][dim]")
     rows, Hq, D = q.shape
-    R = _check_batch(table, length, ell, gamma, row0, rows, dev)
-    _check(q, "q", (rows, Hq, D), (torch.bfloat16,), dev)
-    n_pages = _check_pool(pool, fmt, heads_kv, D, page, dev)
-    out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev) if out is None else out
-    _check(out, "out", (rows, Hq, D), (torch.bfloat16,), dev)
-    if lse is not None:
-        _check(lse, "lse", (rows, Hq), (torch.float32,), dev)
-    _on_current(dev)
+    R, max_pages, p_row0, p_ell, p_len, p_table = _batch(table, length, ell, gamma, row0, rows, dev)
+    p_q = _need(q, "q", (rows, Hq, D), _BF, dev)
+    n_pages, p_pool = _pool(pool, fmt, heads_kv, D, page, dev)
+    if out is None:
+        out = torch.empty((rows, Hq, D), dtype=_BF, device=q.device)
+    p_out = _need(out, "out", (rows, Hq, D), _BF, dev)
+    p_lse = None if lse is None else _need(lse, "lse", (rows, Hq), torch.float32, dev)
+    stream = _raw_stream(dev)
     if rows == 0:
         return out, lse
     ws = _cache_ws(ws, CACHE_WS_ATTENTION, R, gamma, Hq, heads_kv, D, dev)
-    st = lib.dspark_cache_attention(fmt, R, gamma, Hq, heads_kv, D, page, n_pages, table.shape[1], _ptr(q),
-                                    D ** -0.5 if scale is None else scale, window, sinks, _ptr(row0), _ptr(ell),
-                                    _ptr(length), _ptr(table), _ptr(pool), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                    _stream())
+    st = load_library().dspark_cache_attention(fmt, R, gamma, Hq, heads_kv, D, page, n_pages, max_pages, p_q,
+                                               D ** -0.5 if scale is None else scale, window, sinks, p_row0, p_ell,
+                                               p_len, p_table, p_pool, p_out, p_lse, ws.data_ptr(), ws.numel(),
+                                               stream)
     _raise("dspark_cache_attention", st)
     return out, lse
 
@@ -688,45 +701,37 @@ def dspark_cache_read(pool, table, start, count, T, *, fmt, page, heads_kv, dim,
     """k, v [R][T][heads_kv][dim] bf16: cached tokens start[r] .. start[r] +
     count[r] - 1 of every request (start None: 0); rows past count[r] are left
     as they were (of new tensors: zero)."""
-    lib = load_library()
-    dev = pool.device
-    R = table.shape[0]
-    n_pages = _check_pool(pool, fmt, heads_kv, dim, page, dev)
-    _check(table, "table", (R, table.shape[1]), (torch.int32,), dev)
-    if start is not None:
-        _check(start, "start", (R,), (torch.int32,), dev)
-    _check(count, "count", (R,), (torch.int32,), dev)
+    dev = pool.get_device()
+    R, max_pages = table.shape
+    n_pages, p_pool = _pool(pool, fmt, heads_kv, dim, page, dev)
+    p_table = _need(table, "table", (R, max_pages), _I32, dev)
+    p_start = None if start is None else _need(start, "start", (R,), _I32, dev)
+    p_count = _need(count, "count", (R,), _I32, dev)
     shape = (R, T, heads_kv, dim)
-    k = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    _check(k, "k", shape, (torch.bfloat16,), dev)
-    _check(v, "v", shape, (torch.bfloat16,), dev)
-    _on_current(dev)
-    st = lib.dspark_cache_read(fmt, R, T, heads_kv, dim, page, n_pages, table.shape[1], _ptr(start), _ptr(count),
-                               _ptr(table), _ptr(pool), _ptr(k), _ptr(v), _stream())
+    k = torch.zeros(shape, dtype=_BF, device=pool.device) if k is None else k
+    v = torch.zeros(shape, dtype=_BF, device=pool.device) if v is None else v
+    p_k, p_v = _need(k, "k", shape, _BF, dev), _need(v, "v", shape, _BF, dev)
+    st = load_library().dspark_cache_read(fmt, R, T, heads_kv, dim, page, n_pages, max_pages, p_start, p_count, p_table,
+                                          p_pool, p_k, p_v, _raw_stream(dev))
     _raise("dspark_cache_read", st)
     return k, v
 
 
-def _check_pages(table, length, ref, bits, dev):
+def _pages(table, length, ref, bits):
+    """R, max_pages, n_pages, the device, and the addresses of the four."""
+    dev = table.get_device()
     R, max_pages = table.shape
     n_pages = ref.shape[0]
-    i32 = (torch.int32,)
-    _check(table, "table", (R, max_pages), i32, dev)
-    if length is not None:
-        _check(length, "length", (R,), i32, dev)
-    _check(ref, "ref", (n_pages,), i32, dev)
-    _check(bits, "bits", ((n_pages + 31) // 32,), i32, dev)
-    return R, max_pages, n_pages
+    return (R, max_pages, n_pages, dev, _need(table, "table", (R, max_pages), _I32, dev),
+            None if length is None else _need(length, "length", (R,), _I32, dev),
+            _need(ref, "ref", (n_pages,), _I32, dev), _need(bits, "bits", ((n_pages + 31) // 32,), _I32, dev))
 
 
 def dspark_cache_reset(table, length, ref, bits):
     """An empty cache: no pages held, all free.  bits is int32 (the words of
     the bitmap)."""
-    R, max_pages, n_pages = _check_pages(table, length, ref, bits, table.device)
-    _on_current(table.device)
-    st = load_library().dspark_cache_reset(R, n_pages, max_pages, _ptr(table), _ptr(length), _ptr(ref), _ptr(bits),
-                                           _stream())
+    R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    st = load_library().dspark_cache_reset(R, n_pages, max_pages, p_table, p_len, p_ref, p_bits, _raw_stream(dev))
     _raise("dspark_cache_reset", st)
 
 
@@ -735,22 +740,19 @@ def dspark_cache_reserve(table, length, ref, bits, ell, gamma, *, page, ell_out=
     """Pages for rows length[r] .. length[r] + ell[r].  Returns ell_out [R]
     (-1 where a request was refused), pairs [R][2], n_pairs [1] (page copies
     for dspark_cache_copy) and status [1] (0 or ENOPAGES), all int32."""
-    dev = table.device
-    R, max_pages, n_pages = _check_pages(table, length, ref, bits, dev)
-    i32 = dict(dtype=torch.int32, device=dev)
-    _check(ell, "ell", (R,), (torch.int32,), dev)
-    ell_out = torch.empty(R, **i32) if ell_out is None else ell_out
-    pairs = torch.empty((R, 2), **i32) if pairs is None else pairs
-    n_pairs = torch.empty(1, **i32) if n_pairs is None else n_pairs
-    status = torch.empty(1, **i32) if status is None else status
-    for t, name, shape in ((ell_out, "ell_out", (R,)), (pairs, "pairs", (R, 2)), (n_pairs, "n_pairs", (1,)),
-                           (status, "status", (1,))):
-        _check(t, name, shape, (torch.int32,), dev)
-    _on_current(dev)
+    R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    new = lambda *shape: torch.empty(shape, dtype=_I32, device=table.device)
+    p_ell = _need(ell, "ell", (R,), _I32, dev)
+    ell_out = new(R) if ell_out is None else ell_out
+    pairs = new(R, 2) if pairs is None else pairs
+    n_pairs = new(1) if n_pairs is None else n_pairs
+    status = new(1) if status is None else status
+    p_out, p_pairs = _need(ell_out, "ell_out", (R,), _I32, dev), _need(pairs, "pairs", (R, 2), _I32, dev)
+    p_n, p_st = _need(n_pairs, "n_pairs", (1,), _I32, dev), _need(status, "status", (1,), _I32, dev)
+    stream = _raw_stream(dev)
     ws = _cache_ws(ws, CACHE_WS_RESERVE, R, gamma, max_pages, n_pages, 0, dev)
-    st = load_library().dspark_cache_reserve(R, gamma, page, n_pages, max_pages, _ptr(ell), _ptr(length), _ptr(table),
-                                             _ptr(ref), _ptr(bits), _ptr(ell_out), _ptr(pairs), _ptr(n_pairs),
-                                             _ptr(status), _ptr(ws), ws.numel(), _stream())
+    st = load_library().dspark_cache_reserve(R, gamma, page, n_pages, max_pages, p_ell, p_len, p_table, p_ref, p_bits,
+                                             p_out, p_pairs, p_n, p_st, ws.data_ptr(), ws.numel(), stream)
     _raise("dspark_cache_reserve", st)
     return ell_out, pairs, n_pairs, status
 
@@ -758,45 +760,39 @@ def dspark_cache_reserve(table, length, ref, bits, ell, gamma, *, page, ell_out=
 def dspark_cache_commit(table, length, ref, bits, ell, n_acc, gamma, *, page, window=0, sinks=0):
     """Keep rows 0 .. n_acc[r] of every request with ell[r] >= 0; release the
     pages past them and, with a window, those no later row can see."""
-    dev = table.device
-    R, max_pages, n_pages = _check_pages(table, length, ref, bits, dev)
-    _check(ell, "ell", (R,), (torch.int32,), dev)
-    _check(n_acc, "n_acc", (R,), (torch.int32,), dev)
-    _on_current(dev)
-    st = load_library().dspark_cache_commit(R, gamma, page, n_pages, max_pages, window, sinks, _ptr(ell), _ptr(n_acc),
-                                            _ptr(length), _ptr(table), _ptr(ref), _ptr(bits), _stream())
+    R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    st = load_library().dspark_cache_commit(R, gamma, page, n_pages, max_pages, window, sinks,
+                                            _need(ell, "ell", (R,), _I32, dev), _need(n_acc, "n_acc", (R,), _I32, dev),
+                                            p_len, p_table, p_ref, p_bits, _raw_stream(dev))
     _raise("dspark_cache_commit", st)
 
 
 def dspark_cache_fork(table, length, ref, bits, parent, *, page, ws=None):
     """Request r takes over what parent[r] held before the call (r: stays as
     it is; -1: empty)."""
-    dev = table.device
-    R, max_pages, n_pages = _check_pages(table, length, ref, bits, dev)
-    _check(parent, "parent", (R,), (torch.int32,), dev)
-    _on_current(dev)
+    R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    p_parent = _need(parent, "parent", (R,), _I32, dev)
+    stream = _raw_stream(dev)
     ws = _cache_ws(ws, CACHE_WS_FORK, R, 0, max_pages, n_pages, 0, dev)
-    st = load_library().dspark_cache_fork(R, page, n_pages, max_pages, _ptr(parent), _ptr(length), _ptr(table),
-                                          _ptr(ref), _ptr(bits), _ptr(ws), ws.numel(), _stream())
+    st = load_library().dspark_cache_fork(R, page, n_pages, max_pages, p_parent, p_len, p_table, p_ref, p_bits,
+                                          ws.data_ptr(), ws.numel(), stream)
     _raise("dspark_cache_fork", st)
 
 
 def dspark_cache_compact(table, ref, bits, pairs=None, n_pairs=None, ws=None):
     """Pages in use to the low ids; returns pairs [n_pages // 2 or more][2] and
     n_pairs [1] for dspark_cache_copy."""
-    dev = table.device
-    R, max_pages, n_pages = _check_pages(table, None, ref, bits, dev)
-    i32 = dict(dtype=torch.int32, device=dev)
-    pairs = torch.empty((max(1, n_pages // 2), 2), **i32) if pairs is None else pairs
-    n_pairs = torch.empty(1, **i32) if n_pairs is None else n_pairs
-    if pairs.shape[0] < max(1, n_pages // 2):
+    R, max_pages, n_pages, dev, p_table, _, p_ref, p_bits = _pages(table, None, ref, bits)
+    most = max(1, n_pages // 2)
+    pairs = torch.empty((most, 2), dtype=_I32, device=table.device) if pairs is None else pairs
+    n_pairs = torch.empty(1, dtype=_I32, device=table.device) if n_pairs is None else n_pairs
+    if pairs.shape[0] < most:
         raise ValueError(f"pairs: {pairs.shape[0]} rows, n_pages // 2 = {n_pages // 2} may be needed")
-    _check(pairs, "pairs", (pairs.shape[0], 2), (torch.int32,), dev)
-    _check(n_pairs, "n_pairs", (1,), (torch.int32,), dev)
-    _on_current(dev)
+    p_pairs, p_n = _need(pairs, "pairs", (pairs.shape[0], 2), _I32, dev), _need(n_pairs, "n_pairs", (1,), _I32, dev)
+    stream = _raw_stream(dev)
     ws = _cache_ws(ws, CACHE_WS_COMPACT, R, 0, max_pages, n_pages, 0, dev)
-    st = load_library().dspark_cache_compact(R, n_pages, max_pages, _ptr(table), _ptr(ref), _ptr(bits), _ptr(pairs),
-                                             _ptr(n_pairs), _ptr(ws), ws.numel(), _stream())
+    st = load_library().dspark_cache_compact(R, n_pages, max_pages, p_table, p_ref, p_bits, p_pairs, p_n,
+                                             ws.data_ptr(), ws.numel(), stream)
     _raise("dspark_cache_compact", st)
     return pairs, n_pairs
 
@@ -804,16 +800,13 @@ def dspark_cache_compact(table, ref, bits, pairs=None, n_pairs=None, ws=None):
 def dspark_cache_copy(pool, pairs, n_pairs):
     """Page pairs[i][0] to page pairs[i][1], i < n_pairs, in a pool [n_pages]
     [page bytes] or in every layer of [layers][n_pages][page bytes]."""
-    dev = pool.device
-    if pool.dim() == 2:
-        pool = pool[None]
-    if pool.dim() != 3:
+    dev = pool.get_device()
+    if pool.dim() not in (2, 3):
         raise ValueError("pool must be [n_pages][page bytes] or [layers][n_pages][page bytes]")
-    layers, n_pages, nb = pool.shape
-    _check(pool, "pool", (layers, n_pages, nb), (torch.uint8,), dev)
-    _check(pairs, "pairs", (pairs.shape[0], 2), (torch.int32,), dev)
-    _check(n_pairs, "n_pairs", (1,), (torch.int32,), dev)
-    _on_current(dev)
-    st = load_library().dspark_cache_copy(layers, n_pages * nb, nb, n_pages, _ptr(pairs), _ptr(n_pairs),
-                                          pairs.shape[0], _ptr(pool), _stream())
+    layers = pool.shape[0] if pool.dim() == 3 else 1
+    n_pages, nb = pool.shape[-2:]
+    p_pool = _need(pool, "pool", pool.shape, _U8, dev)
+    p_pairs, p_n = _need(pairs, "pairs", (pairs.shape[0], 2), _I32, dev), _need(n_pairs, "n_pairs", (1,), _I32, dev)
+    st = load_library().dspark_cache_copy(layers, n_pages * nb, nb, n_pages, p_pairs, p_n, pairs.shape[0], p_pool,
+                                          _raw_stream(dev))
     _raise("dspark_cache_copy", st)
