@@ -103,7 +103,6 @@ __device__ __forceinline__ uint32_t code_of(T x, T one) {
   return c | (x < 0 ? 8u : 0u);
 }
 
-template <int D>
 __device__ __forceinline__ void unpack(const u32x4& v, float (&x)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32(static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1))));
@@ -140,84 +139,81 @@ __device__ __forceinline__ void store_k_fp4(const double (&x)[8], int li, char* 
   if ((li & 3) == 0) head[L::k_scale(P, t) + li / 4] = static_cast<char>(bad ? 255 : e2 + 127);
 }
 
-// V of the group's tokens for one head.  valid: bit j = token j of the
-// aligned group of 8 is new; t8: the group's first token in its page.
-template <int FMT, int D>
-__device__ __forceinline__ void store_v(const AppendArgs& a, int h, int li, int64_t row_first, int first, int n,
-                                        char* head, int t8) {
-  typedef PageLayout<FMT, D> L;
+// V of one head of a 16-bit page: all 8 tokens of the group, transposed in
+// registers so that every store is a dim's 16 bytes ..
+template <int D>
+__device__ __forceinline__ void store_v8_bf16(const uint16_t* src, int64_t ldv, char* dst) {
+  u32x4 x[kGroup];
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j) x[j] = *reinterpret_cast<const u32x4*>(src + j * ldv);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = __builtin_amdgcn_perm(x[2 * j + 1][e / 2], x[2 * j][e / 2], (e & 1) ? 0x07060302u : 0x05040100u);
+    *reinterpret_cast<u32x4*>(dst + 16 * e) = w;
+  }
+}
+
+// .. or one token, whose neighbours in those 16 bytes stay as they are.
+__device__ __forceinline__ void store_v1_bf16(const uint16_t* src, char* dst) {
+  const u32x4 x = *reinterpret_cast<const u32x4*>(src);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    *reinterpret_cast<uint16_t*>(dst + 16 * e) = static_cast<uint16_t>(x[e / 2] >> (16 * (e & 1)));
+}
+
+// V of one head of a 4-bit page: tokens first .. first + n - 1 of the group
+// of 8 at src, a dim's 8 codes in one word; words with other tokens in them
+// are read and merged.
+template <int D>
+__device__ __forceinline__ void store_v_fp4(const uint16_t* src, int64_t ldv, int li, int first, int n, char* head,
+                                            int P, int t8) {
+  typedef PageLayout<DSPARK_CACHE_FP4, D> L;
   u32x4 x[kGroup];
 #pragma unroll
   for (int j = 0; j < kGroup; ++j) {
     x[j] = u32x4{0u, 0u, 0u, 0u};
-    if (j >= first && j < first + n)
-      x[j] = *reinterpret_cast<const u32x4*>(a.v + (row_first + j - first) * a.ldv + static_cast<int64_t>(h) * D +
-                                             li * 8);
+    if (j >= first && j < first + n) x[j] = *reinterpret_cast<const u32x4*>(src + (j - first) * ldv);
   }
-  if constexpr (FMT == DSPARK_CACHE_BF16) {
-    if (n == kGroup) {
+  uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        u32x4 w;
+  for (int e = 0; e < 8; ++e) w[e] = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = (x[2 * j][e / 2] >> (16 * (e & 1))) & 0xFFFFu;
-          const uint32_t hi = (x[2 * j + 1][e / 2] >> (16 * (e & 1))) & 0xFFFFu;
-          w[j] = lo | hi << 16;
-        }
-        *reinterpret_cast<u32x4*>(head + L::v(a.P, t8, li * 8 + e)) = w;
-      }
-    } else {
-      // the other tokens of the words stay: two-byte stores
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j)
-        if (j >= first && j < first + n) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint16_t*>(head + L::v(a.P, t8, li * 8 + e) + 2 * j) =
-                static_cast<uint16_t>(x[j][e / 2] >> (16 * (e & 1)));
-        }
-    }
-  } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 0;
-#pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      float f[8], top = 0.f;
-      bool bad = false;
-      unpack<D>(x[j], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        top = fmaxf(top, fabsf(f[e]));
-        bad |= !(fabsf(f[e]) <= 3.4028234e38f);
-      }
-#pragma unroll
-      for (int o = 1; o < D / 8; o <<= 1) {
-        top = fmaxf(top, __shfl_xor(top, o));
-        bad |= __shfl_xor(static_cast<int>(bad), o) != 0;
-      }
-      // 6 |v| against the borders times max |v|: products of 16-bit values
-      // with numbers of at most 3 bits, exact in fp32; above 2^100 both sides
-      // are scaled down first so that they stay finite
-      const float sc = top > 1.2676506e30f ? 7.8886091e-31f : 1.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        w[e] |= (bad || top == 0.f ? 0u : code_of(6.f * (f[e] * sc), top * sc)) << (4 * j);
-      if (li == 0 && j >= first && j < first + n)
-        *reinterpret_cast<float*>(head + L::v_scale(a.P, t8 + j)) = bad ? __builtin_nanf("") : top / 6.f;
-    }
-    const uint32_t keep = ~static_cast<uint32_t>(((1ull << (4 * n)) - 1ull) << (4 * first));
+  for (int j = 0; j < kGroup; ++j) {
+    if (j < first || j >= first + n) continue;  // the same for all lanes of the head
+    float f[8], top = 0.f;
+    bool bad = false;
+    unpack(x[j], f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(head + L::v(a.P, t8, li * 8 + e));
-      *p = n == kGroup ? w[e] : (*p & keep) | (w[e] & ~keep);
+      top = fmaxf(top, fabsf(f[e]));
+      bad |= !(fabsf(f[e]) <= 3.4028234e38f);
     }
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1) {
+      top = fmaxf(top, __shfl_xor(top, o));
+      bad |= __shfl_xor(static_cast<int>(bad), o) != 0;
+    }
+    // 6 |v| against the borders times max |v|: products of 16-bit values with
+    // numbers of at most 3 bits, exact in fp32; above 2^100 both sides are
+    // scaled down first so that they stay finite
+    const float sc = top > 1.2676506e30f ? 7.8886091e-31f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      w[e] |= (bad || top == 0.f ? 0u : code_of(6.f * (f[e] * sc), top * sc)) << (4 * j);
+    if (li == 0) *reinterpret_cast<float*>(head + L::v_scale(P, t8 + j)) = bad ? __builtin_nanf("") : top / 6.f;
   }
+  const uint32_t mine = static_cast<uint32_t>(((1ull << (4 * n)) - 1ull) << (4 * first));
+  // dims 8 li .. of a group of 32: consecutive in the first of the two dim axes
+  uint32_t* p = reinterpret_cast<uint32_t*>(head + L::v(P, t8, li * 8));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e * L::E] = n == kGroup ? w[e] : (p[e * L::E] & ~mine) | w[e];
 }
 
 template <int FMT, int D>
-__global__ __launch_bounds__(kThreads) void cache_append_kernel(AppendArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void cache_append_kernel(AppendArgs a) {
   constexpr int L = D / 8, kHeads = kThreads / L;  // head slots of the work group
   // keys of 4-bit pages need fp64 sines as well
   __shared__ float cs[kGroup * D];
@@ -240,9 +236,30 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(AppendArgs a) {
   const int t8 = static_cast<int>(base % a.P);
   char* page = id >= 0 ? a.pool + id * a.page_bytes : nullptr;
 
+  // a unit is one head of one row (q, k, and V one row at a time), or V of a
+  // head for a whole group; every lane of a head slot takes the same unit, so
+  // the shuffles inside a head are whole
+  const int li = threadIdx.x % L;
+  const int per_row = a.Hq + a.Hkv;
+  const bool whole = FMT == DSPARK_CACHE_FP4 || n == kGroup;
+  const int units = n * per_row + (whole ? a.Hkv : n * a.Hkv);
+  int u = blockIdx.y * kHeads + threadIdx.x / L;
+  // V and the first row need no angles: they are on their way while those are made
+  auto row_of = [&](int unit, const uint16_t** src) {
+    const int j = unit / per_row, head = unit - j * per_row;
+    *src = head < a.Hq ? a.q + (row_first + j) * a.ldq + head * D
+                       : a.k + (row_first + j) * a.ldk + (head - a.Hq) * D;
+    return j;
+  };
+  u32x4 raw{0u, 0u, 0u, 0u};
+  if (u < n * per_row) {
+    const uint16_t* src;
+    row_of(u, &src);
+    raw = *reinterpret_cast<const u32x4*>(src + li * 8);
+  }
   const int half = a.rot / 2;
   for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int row = i / half, p = i % half;
+    const int row = i / half, p = i - row * half;
     const double turns = static_cast<double>(t0 + row) * a.freq[p] * 0.15915494309189535;
     const double t = turns - rint(turns);
     if constexpr (FMT == DSPARK_CACHE_FP4) {
@@ -261,26 +278,36 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(AppendArgs a) {
   }
   __syncthreads();
 
-  const int li = threadIdx.x % L;
-  const int per_row = a.Hq + a.Hkv;
-  const int units = n * per_row + a.Hkv;
-  // every lane of a head slot takes the same unit, so the shuffles inside a head are whole
-  for (int u = blockIdx.y * kHeads + threadIdx.x / L; u < units; u += gridDim.y * kHeads) {
+#pragma unroll 1
+  for (; u < units; u += gridDim.y * kHeads) {
     if (u >= n * per_row) {
-      const int h = u - n * per_row;
-      if (page) store_v<FMT, D>(a, h, li, row_first, first, n, page + h * PageLayout<FMT, D>::head_bytes(a.P), t8);
+      const int v = u - n * per_row;
+      const int h = whole ? v : v % a.Hkv, j = whole ? 0 : v / a.Hkv;
+      const uint16_t* src = a.v + (row_first + j) * a.ldv + static_cast<int64_t>(h) * D + li * 8;
+      if (!page) continue;
+      char* head = page + h * PageLayout<FMT, D>::head_bytes(a.P);
+      if constexpr (FMT == DSPARK_CACHE_BF16) {
+        char* dst = head + PageLayout<FMT, D>::v(a.P, t8, li * 8);
+        if (whole) store_v8_bf16<D>(src, a.ldv, dst);
+        else store_v1_bf16(src, dst + 2 * (first + j));
+      } else {
+        store_v_fp4<D>(src, a.ldv, li, first, n, head, a.P, t8);
+      }
       continue;
     }
-    const int j = u / per_row, head = u % per_row;
-    const int64_t row = row_first + j;
+    const uint16_t* src;
+    const int j = row_of(u, &src), head = u - j * per_row;
     const bool is_q = head < a.Hq;
-    const uint16_t* src = is_q ? a.q + row * a.ldq + static_cast<int64_t>(head) * D
-                               : a.k + row * a.ldk + static_cast<int64_t>(head - a.Hq) * D;
-    const u32x4 raw = *reinterpret_cast<const u32x4*>(src + li * 8);
+    const u32x4 now = raw;
+    const int next = u + gridDim.y * kHeads;
+    if (next < n * per_row) {
+      row_of(next, &src);
+      raw = *reinterpret_cast<const u32x4*>(src + li * 8);
+    }
     if constexpr (FMT == DSPARK_CACHE_FP4) {
       if (!is_q) {
         float f[8];
-        unpack<D>(raw, f);
+        unpack(now, f);
         double x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = f[e];
@@ -291,11 +318,11 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(AppendArgs a) {
       }
     }
     float x[8];
-    unpack<D>(raw, x);
+    unpack(now, x);
     norm_rotate<float, D>(x, li, is_q ? a.wq : a.wk, a.eps, a.rot, a.adjacent != 0, cs + j * D);
     const u32x4 y = pack_bf16(x);
     if (is_q) {
-      *reinterpret_cast<u32x4*>(a.q_out + (row * a.Hq + head) * D + li * 8) = y;
+      *reinterpret_cast<u32x4*>(a.q_out + ((row_first + j) * a.Hq + head) * D + li * 8) = y;
     } else if (page) {
       char* hp = page + (head - a.Hq) * PageLayout<FMT, D>::head_bytes(a.P);
       if constexpr (FMT == DSPARK_CACHE_BF16)
@@ -388,7 +415,7 @@ hipError_t append_run(AppendArgs& a, hipStream_t s) {
   const int64_t gx = static_cast<int64_t>(a.R) * a.groups;
   // enough work groups along the heads to fill the device when there are few token groups
   const int most = ceil_div(kGroup * (a.Hq + a.Hkv) + a.Hkv, kHeads);
-  const int64_t want = 8LL * compute_units() / gx;
+  const int64_t want = 16LL * compute_units() / gx;
   const int gy = want < 1 ? 1 : want > most ? most : static_cast<int>(want);
   cache_append_kernel<FMT, D><<<dim3(static_cast<unsigned>(gx), gy), kThreads, 0, s>>>(a);
   return hipGetLastError();

@@ -60,8 +60,11 @@ struct Shape {
 
 // What a work group leaves for the join: the part it opened but did not close.
 struct Desc {
-  int parts;   // 0: nothing
-  int r, block, head;
+  int parts;     // 0: nothing
+  int rows, m0;  // the row block
+  int head;
+  int64_t first_row;  // the request's row 0 in q and out
+  int64_t pad;
 };
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 x) {
@@ -136,6 +139,10 @@ struct KTile;
 template <int FMT, int D>
 struct VTile;
 
+// Keeps a rare branch a branch: without it the compiler turns the few
+// instructions inside into selects that every tile pays for.
+__device__ __forceinline__ void rare() { asm volatile(""); }
+
 template <int D>
 struct KTile<DSPARK_CACHE_BF16, D> {
   u32x4 x[D / 16];
@@ -145,11 +152,12 @@ struct KTile<DSPARK_CACHE_BF16, D> {
     for (int u = 0; u < D / 16; ++u) x[u] = *reinterpret_cast<const u32x4*>(p + u * 512);
   }
   static __device__ __forceinline__ int q_dim(int u, int h) { return 16 * u + 8 * h; }
-  __device__ __forceinline__ f32x16 scores(const u32x4 (&q)[D / 16], int) const {
+  template <typename Q>
+  __device__ __forceinline__ f32x16 scores(const Q& q, int) const {
     f32x16 s = {0.f};
 #pragma unroll
     for (int u = 0; u < D / 16; ++u)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(x[u]), as_bf16(q[u]), s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(x[u]), as_bf16(q(u)), s, 0, 0, 0);
     return s;
   }
 };
@@ -175,7 +183,8 @@ struct KTile<DSPARK_CACHE_FP4, D> {
     }
   }
   static __device__ __forceinline__ int q_dim(int u, int h) { return 32 * (2 * (u / 4) + h) + 8 * (u % 4); }
-  __device__ __forceinline__ f32x16 scores(const u32x4 (&q)[D / 16], int h) const {
+  template <typename Q>
+  __device__ __forceinline__ f32x16 scores(const Q& q, int h) const {
     f32x16 s = {0.f};
     bool bad = false;
 #pragma unroll
@@ -187,12 +196,13 @@ struct KTile<DSPARK_CACHE_FP4, D> {
       for (int v = 0; v < 4; ++v) {
         const uint32_t w = x[g][v];
         const u32x4 k{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale), fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)};
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(k), as_bf16(q[4 * g + v]), s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(k), as_bf16(q(4 * g + v)), s, 0, 0, 0);
       }
     }
     // a NaN scale makes its token's scores NaN: slot r is accumulator j of half h with 8 (j / 4) + 4 h + j % 4 = r
     const unsigned long long rows = __ballot(bad);
     if (rows) {
+      rare();
       const uint32_t r = static_cast<uint32_t>(rows) | static_cast<uint32_t>(rows >> 32);
 #pragma unroll
       for (int j = 0; j < 16; ++j)
@@ -212,6 +222,7 @@ struct VTile<DSPARK_CACHE_BF16, D> {
   }
   __device__ __forceinline__ u32x4 operand(int s, int b) const { return x[s][b]; }
   __device__ __forceinline__ float weight(int, float p) const { return p; }
+  __device__ __forceinline__ void hide(int, bool) {}
 };
 
 // 4 bits: a token's scale goes into its weights.
@@ -243,6 +254,11 @@ struct VTile<DSPARK_CACHE_FP4, D> {
     return u32x4{fp4_pair<0>(w, 1.f), fp4_pair<1>(w, 1.f), fp4_pair<2>(w, 1.f), fp4_pair<3>(w, 1.f)};
   }
   __device__ __forceinline__ float weight(int j, float p) const { return p * sc[j / 8][(j % 8) / 4][j % 4]; }
+  // a hidden token's scale may be anything, its weight is zero
+  __device__ __forceinline__ void hide(int j, bool see) {
+    f32x4& x = sc[j / 8][(j % 8) / 4];
+    x[j % 4] = see ? x[j % 4] : 0.f;
+  }
 };
 
 // Running softmax of a lane's query row (m is the row's, l the lane's own
@@ -311,6 +327,10 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
   typedef PageLayout<FMT, D> L;
   constexpr int W = Shape<D>::kWaves, T = W * 64, NB = D / 32, KS = D / 16;
   constexpr float kSlack = 8.f;  // a weight may reach 2^8 before the sums are rescaled
+  // heads of 256 dims: the output alone takes 128 registers and a tile 128,
+  // so the query rows go to LDS
+  constexpr bool kQueryInLds = D == 256;
+  __shared__ u32x4 lds_q[kQueryInLds ? W : 1][kQueryInLds ? KS : 1][64];
   __shared__ f32x4 lds_o[W / 2][NB * 4][64];
   __shared__ float2 lds_ml[W / 2][64];
   __shared__ int64_t lds_scan[W];
@@ -369,7 +389,7 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
     }
   }
   __syncthreads();
-  Desc left{0, 0, 0, 0};
+  Desc left{};
   int entry = u0 < u1 ? __builtin_amdgcn_readfirstlane(lds_entry) : 0;
   int64_t base = u0 < u1 ? lds_base : 0;
 
@@ -417,13 +437,20 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
 
     const int steps = active && t0 + wt < t1 ? (t1 - t0 - wt + WT - 1) >> (__ffs(WT) - 1) : 0;
     if (steps > 0) {
-      u32x4 q[KS];
+      // the query rows' operands: in registers, or the wave's own slice of LDS
+      u32x4 q_reg[kQueryInLds ? 1 : KS];
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        q[x] = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
+        u32x4 v = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
 #pragma unroll
-        for (int y = 0; y < 4; ++y) q[x][y] = (q[x][y] & a.q_keep) ^ a.q_flip;
+        for (int y = 0; y < 4; ++y) v[y] = (v[y] & a.q_keep) ^ a.q_flip;
+        if constexpr (kQueryInLds) lds_q[wave][x][lane] = v;
+        else q_reg[x] = v;
       }
+      auto q = [&](int x) {
+        if constexpr (kQueryInLds) return lds_q[wave][x][lane];
+        else return q_reg[x];
+      };
       const char* pool = a.pool + hk * L::head_bytes(a.P);
       const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
       const int lp = 31 - __clz(a.P);
@@ -477,15 +504,14 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
         if ((k & 63) == 63) fetch_ids(next);
         aim(next);
         load_k();
-        uint32_t visible = 0xFFFFu;
         if (!clear) {
-          visible = 0;
+          rare();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int t = ct + 16 * (j / 8) + 8 * h + j % 8;
             const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
             s[j] = see ? s[j] : neg_inf();
-            visible |= static_cast<uint32_t>(see) << j;
+            vt.hide(j, see);
           }
         }
         float top = s[0];
@@ -515,14 +541,10 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
 #pragma unroll
         for (int j = 0; j < 16; j += 2) pk[j / 8][(j % 8) / 2] = bf16_pair(vt.weight(j, p[j]), vt.weight(j + 1, p[j + 1]));
         bool odd = false;
-        if (!clear) {
-          if constexpr (FMT == DSPARK_CACHE_FP4) {  // a hidden token's scale may be anything
-#pragma unroll
-            for (int j = 0; j < 16; j += 2)
-              pk[j / 8][(j % 8) / 2] &=
-                  ((visible >> j) & 1u ? 0xFFFFu : 0u) | ((visible >> (j + 1)) & 1u ? 0xFFFF0000u : 0u);
-          } else {
+        if constexpr (FMT == DSPARK_CACHE_BF16) {
+          if (!clear) {
             // tokens that no row of the wave sees become zeros; of the others, values that are not finite too
+            rare();
 #pragma unroll
             for (int s2 = 0; s2 < 2; ++s2) {
               u32x4 keep{0u, 0u, 0u, 0u};
@@ -551,8 +573,16 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
             acc.o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vt.operand(s2, x)), as_bf16(pk[s2]), acc.o[x], 0,
                                                                0, 0);
         if constexpr (FMT == DSPARK_CACHE_BF16)
-          if (__any(odd))
+          if (__any(odd)) {
+            uint32_t visible = 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int t = ct + 16 * (j / 8) + 8 * h + j % 8;
+              const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
+              visible |= static_cast<uint32_t>(see) << j;
+            }
             add_non_finite<D>(acc.o, p, visible, ch0, ch1, a.P, ct & (a.P - 1), (ct + 16) & (a.P - 1), lane);
+          }
         load_v();
       }
     }
@@ -617,41 +647,58 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
       }
     }
     if (opens && !closes)  // the work group that holds the last tile's first unit has the last part
-      left = Desc{deal.owner(seg_end - weight) - wg + 1, r, entry - r * a.blocks, hk};
+      left = Desc{deal.owner(seg_end - weight) - wg + 1, b.rows, b.m0, hk, first_row, 0};
   }
   if (threadIdx.x == 0) reinterpret_cast<Desc*>(a.desc)[wg] = left;
 }
 
-// Joins the parts of what work group blockIdx.x opened and did not close, in
-// the order of the tokens.  A thread takes four output dims of one row.
+// Joins the parts of what a work group opened and did not close, in the order
+// of the tokens.  A wave takes 4 output dims of 32 rows per half (a piece, as
+// the parts were stored).  The pieces of one work group are consecutive
+// blocks, so that they spread over the dies: what is left open is often a few
+// work groups whose indices are multiples of 8.
 template <int FMT, int D>
 __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
-  constexpr int W = Shape<D>::kWaves, NB = D / 32;
-  const int wg = blockIdx.x;
+  constexpr int NB = D / 32;
+  const int wg = blockIdx.x / (a.slot_tiles * NB);
   const Desc d = reinterpret_cast<const Desc*>(a.desc)[wg];
   if (d.parts == 0) return;
-  const Block b = block_of(a, d.r * a.blocks + d.block, W * kTile);
-  const int piece = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int piece = (blockIdx.x % (a.slot_tiles * NB)) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wq = piece / (NB * 4), x = piece % (NB * 4);
   const int row = wq * kTile + (lane & 31);
-  if (row >= b.rows) return;
+  if (wq * kTile >= d.rows) return;
   float m = neg_inf(), l = 0.f;
   f32x4 o{0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < d.parts; ++k) {
-    const int64_t slot = (static_cast<int64_t>(wg + k) * 2 + (k == 0 ? 1 : 0)) * a.slot_tiles + wq;
-    const float2 ml = a.ml[slot * kTile + (lane & 31)];
-    const f32x4 y = reinterpret_cast<const f32x4*>(a.part)[slot * (NB * 4 * 64) + x * 64 + lane];
-    const float top = fmaxf(m, ml.x), ref = top == neg_inf() ? 0.f : top;
-    const float sa = __builtin_amdgcn_exp2f(m - ref), sb = __builtin_amdgcn_exp2f(ml.x - ref);
-    m = top;
-    l = l * sa + ml.y * sb;
+  // four parts' loads at a time: the loop is a chain of latencies otherwise
+  constexpr int kBatch = 4;
+#pragma unroll 1
+  for (int k0 = 0; k0 < d.parts; k0 += kBatch) {
+    float2 ml[kBatch];
+    f32x4 y[kBatch];
 #pragma unroll
-    for (int z = 0; z < 4; ++z) o[z] = o[z] * sa + y[z] * sb;
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = k0 + j;
+      ml[j] = make_float2(neg_inf(), 0.f);
+      y[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (k < d.parts) {
+        const int64_t slot = (static_cast<int64_t>(wg + k) * 2 + (k == 0 ? 1 : 0)) * a.slot_tiles + wq;
+        ml[j] = a.ml[slot * kTile + (lane & 31)];
+        y[j] = reinterpret_cast<const f32x4*>(a.part)[slot * (NB * 4 * 64) + x * 64 + lane];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float top = fmaxf(m, ml[j].x), ref = top == neg_inf() ? 0.f : top;
+      const float sa = __builtin_amdgcn_exp2f(m - ref), sb = __builtin_amdgcn_exp2f(ml[j].x - ref);
+      m = top;
+      l = l * sa + ml[j].y * sb;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) o[z] = o[z] * sa + y[j][z] * sb;
+    }
   }
-  const int G = a.G;
-  const int i = (b.m0 + row) / G, g = (b.m0 + row) % G;
-  const int64_t first_row = a.row0 ? static_cast<int64_t>(a.row0[d.r]) : static_cast<int64_t>(d.r) * (a.gamma + 1);
-  const int64_t out_at = (first_row + i) * a.Hq + d.head * G + g;
+  if (row >= d.rows) return;
+  const int i = (d.m0 + row) / a.G, g = (d.m0 + row) - i * a.G;
+  const int64_t out_at = (d.first_row + i) * a.Hq + d.head * a.G + g;
   const float inv = l != 0.f ? 1.f / l : 0.f;
   const u32x2 w{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
   *reinterpret_cast<u32x2*>(a.out + out_at * D + (x / 4) * 32 + 8 * (x % 4) + 4 * (lane >> 5)) = w;
@@ -689,7 +736,7 @@ hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
   cache_attention_tiles<FMT, D><<<grid, W * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  cache_attention_join<FMT, D><<<dim3(grid, a.slot_tiles * NB), 256, 0, s>>>(a);
+  cache_attention_join<FMT, D><<<grid * a.slot_tiles * NB, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
