@@ -51,13 +51,6 @@ struct AttnArgs {
   float* part;
 };
 
-template <int D>
-struct Shape {
-  static constexpr int kWaves = D == 256 ? 4 : 8;
-  static constexpr int kSteps = D / 16;      // products of a tile's scores
-  static constexpr int kBlocks = D / 32;     // 32-dim blocks of the output
-};
-
 // What a work group leaves for the join: the part it opened but did not close.
 struct Desc {
   int parts;     // 0: nothing
@@ -269,15 +262,6 @@ struct Acc {
   f32x16 o[D / 32];
 };
 
-template <int D>
-__device__ __forceinline__ void join(Acc<D>& a, float m, float l, float* scale_a, float* scale_b) {
-  const float top = fmaxf(a.m, m), base = top == neg_inf() ? 0.f : top;
-  *scale_a = __builtin_amdgcn_exp2f(a.m - base);
-  *scale_b = __builtin_amdgcn_exp2f(m - base);
-  a.l = a.l * *scale_a + l * *scale_b;
-  a.m = top;
-}
-
 // A visible value that is not finite in a tile that some rows see and others
 // do not: the products above took it as zero, because zero weights times an
 // infinity are NaN; here each row adds what it does see.  Rare and slow.
@@ -322,17 +306,20 @@ struct Deal {
   }
 };
 
-template <int FMT, int D>
-__global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(AttnArgs a) {
+// W waves: 256 registers a wave for heads of 64 and 128 dims, so 8 waves a
+// compute unit, as one work group or two; 512 and 4 waves for 256 dims.
+template <int FMT, int D, int W>
+__global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tiles(AttnArgs a) {
   typedef PageLayout<FMT, D> L;
-  constexpr int W = Shape<D>::kWaves, T = W * 64, NB = D / 32, KS = D / 16;
+  constexpr int T = W * 64, NB = D / 32, KS = D / 16;
   constexpr float kSlack = 8.f;  // a weight may reach 2^8 before the sums are rescaled
   // heads of 256 dims: the output alone takes 128 registers and a tile 128,
   // so the query rows go to LDS
   constexpr bool kQueryInLds = D == 256;
-  __shared__ u32x4 lds_q[kQueryInLds ? W : 1][kQueryInLds ? KS : 1][64];
-  __shared__ f32x4 lds_o[W / 2][NB * 4][64];
-  __shared__ float2 lds_ml[W / 2][64];
+  // (the wave's own, under its output, which it writes when done with them)
+  __shared__ f32x4 lds_own[W][NB * 4][64];
+  __shared__ float2 lds_ml[W][64];
+  static_assert(NB * 4 >= KS && (NB * 4) % W == 0, "the queries fit under the output; waves share its pieces");
   __shared__ int64_t lds_scan[W];
   __shared__ int64_t lds_base;
   __shared__ int lds_entry;
@@ -352,6 +339,7 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
   int nb = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1 && per == 1) break;
     int64_t sum = 0;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
@@ -386,6 +374,10 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
       deal.rest = N - deal.share * nb;
       u0 = deal.begin(wg);
       u1 = wg < nb ? deal.begin(wg + 1) : u0;
+      if (per == 1 && u0 >= at && u0 < at + sum) {
+        lds_entry = e0;
+        lds_base = at;
+      }
     }
   }
   __syncthreads();
@@ -444,11 +436,11 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
         u32x4 v = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
 #pragma unroll
         for (int y = 0; y < 4; ++y) v[y] = (v[y] & a.q_keep) ^ a.q_flip;
-        if constexpr (kQueryInLds) lds_q[wave][x][lane] = v;
+        if constexpr (kQueryInLds) lds_own[wave][x][lane] = __builtin_bit_cast(f32x4, v);
         else q_reg[x] = v;
       }
       auto q = [&](int x) {
-        if constexpr (kQueryInLds) return lds_q[wave][x][lane];
+        if constexpr (kQueryInLds) return __builtin_bit_cast(u32x4, lds_own[wave][x][lane]);
         else return q_reg[x];
       };
       const char* pool = a.pool + hk * L::head_bytes(a.P);
@@ -587,65 +579,60 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
       }
     }
 
-    // join the waves along the tokens, halving
-#pragma unroll 1
-    for (int step = WT / 2; step >= 1; step >>= 1) {
-      if (active && wt >= step && wt < 2 * step) {
-        const int slot = (wt - step) * qt + wq;
-        lds_ml[slot][lane] = make_float2(acc.m, acc.l);
-#pragma unroll
-        for (int x = 0; x < NB; ++x)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            lds_o[slot][x * 4 + j][lane] =
-                f32x4{acc.o[x][4 * j], acc.o[x][4 * j + 1], acc.o[x][4 * j + 2], acc.o[x][4 * j + 3]};
-      }
-      __syncthreads();
-      if (active && wt < step) {
-        const int slot = wt * qt + wq;
-        const float2 ml = lds_ml[slot][lane];
-        float sa, sb;
-        join<D>(acc, ml.x, ml.y, &sa, &sb);
-#pragma unroll
-        for (int x = 0; x < NB; ++x)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4 y = lds_o[slot][x * 4 + j][lane];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) acc.o[x][4 * j + z] = acc.o[x][4 * j + z] * sa + y[z] * sb;
-          }
-      }
-      __syncthreads();
-    }
-
+    // Join the waves along the tokens and write: every wave leaves its output
+    // in LDS and takes an equal share of its rows' dims from all of them.
     const bool opens = t0 == 0, closes = t1 == b.count;
-    if (active && wt == 0) {
-      const float l = acc.l + xor32(acc.l);
-      if (opens && closes) {
-        if (wq * kTile + col < b.rows) {
-          const float inv = l != 0.f ? 1.f / l : 0.f;
+    const bool valid = wq * kTile + col < b.rows;
+    const int64_t slot = (static_cast<int64_t>(wg) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
+    if (active) lds_ml[wave][lane] = make_float2(acc.m, acc.l);
+    __syncthreads();
+    const bool whole = opens && closes;
+    float m = acc.m, l = 0.f;
+    if (active) {
+      float2 ml[W];
 #pragma unroll
-          for (int x = 0; x < NB; ++x)
+      for (int k = 0; k < W; ++k) ml[k] = k < WT ? lds_ml[wq + k * qt][lane] : make_float2(neg_inf(), 0.f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const u32x2 w{bf16_pair(acc.o[x][4 * j] * inv, acc.o[x][4 * j + 1] * inv),
-                            bf16_pair(acc.o[x][4 * j + 2] * inv, acc.o[x][4 * j + 3] * inv)};
-              *reinterpret_cast<u32x2*>(a.out + out_at * D + x * 32 + 8 * j + 4 * h) = w;
-            }
-          if (a.lse && h == 0) a.lse[out_at] = l != 0.f ? (acc.m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
+      for (int k = 0; k < W; ++k) m = fmaxf(m, ml[k].x);
+      const float ref = m == neg_inf() ? 0.f : m;
+#pragma unroll
+      for (int k = 0; k < W; ++k) l += ml[k].y * __builtin_amdgcn_exp2f(ml[k].x - ref);
+      l += xor32(l);
+      const float f = __builtin_amdgcn_exp2f(acc.m - ref) * (!whole ? 1.f : l != 0.f ? 1.f / l : 0.f);
+#pragma unroll
+      for (int x = 0; x < NB; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          lds_own[wave][x * 4 + j][lane] = f32x4{acc.o[x][4 * j] * f, acc.o[x][4 * j + 1] * f,
+                                                 acc.o[x][4 * j + 2] * f, acc.o[x][4 * j + 3] * f};
+    }
+    __syncthreads();
+    if (active) {
+      // piece x: dims 32 (x / 4) + 8 (x % 4) + 4 h .. of the lane's row
+      const int share = NB * 4 >> (__ffs(WT) - 1);
+#pragma unroll 2
+      for (int x = wt * share; x < (wt + 1) * share; ++x) {
+        f32x4 o{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+          if (k < WT) {
+            const f32x4 y = lds_own[wq + k * qt][x][lane];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) o[z] += y[z];
+          }
+        if (!whole) {
+          if (valid) reinterpret_cast<f32x4*>(a.part)[(slot * (NB * 4) + x) * 64 + lane] = o;
+        } else if (valid) {
+          const u32x2 w{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+          *reinterpret_cast<u32x2*>(a.out + out_at * D + (x / 4) * 32 + 8 * (x % 4) + 4 * h) = w;
         }
-      } else {
-        const int64_t slot = (static_cast<int64_t>(wg) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
-        if (h == 0) a.ml[slot * kTile + col] = make_float2(acc.m, l);
-        f32x4* dst = reinterpret_cast<f32x4*>(a.part) + slot * (NB * 4 * 64);
-#pragma unroll
-        for (int x = 0; x < NB; ++x)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dst[(x * 4 + j) * 64 + lane] =
-                f32x4{acc.o[x][4 * j], acc.o[x][4 * j + 1], acc.o[x][4 * j + 2], acc.o[x][4 * j + 3]};
+      }
+      if (wt == 0 && h == 0) {
+        if (!whole) a.ml[slot * kTile + col] = make_float2(m, l);
+        else if (a.lse && valid) a.lse[out_at] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
       }
     }
+    __syncthreads();  // before the next segment's waves write there
     if (opens && !closes)  // the work group that holds the last tile's first unit has the last part
       left = Desc{deal.owner(seg_end - weight) - wg + 1, b.rows, b.m0, hk, first_row, 0};
   }
@@ -654,25 +641,40 @@ __global__ __launch_bounds__(Shape<D>::kWaves * 64) void cache_attention_tiles(A
 
 // Joins the parts of what a work group opened and did not close, in the order
 // of the tokens.  A wave takes 4 output dims of 32 rows per half (a piece, as
-// the parts were stored).  The pieces of one work group are consecutive
-// blocks, so that they spread over the dies: what is left open is often a few
-// work groups whose indices are multiples of 8.
-template <int FMT, int D>
+// the parts were stored); with many parts (SPLIT 4) the four waves of a block
+// take a quarter of one piece's parts each.  The pieces of one work group are
+// consecutive blocks, so that they spread over the dies: what is left open is
+// often a few work groups whose indices are multiples of 8.
+template <int D, int SPLIT>
 __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
   constexpr int NB = D / 32;
-  const int wg = blockIdx.x / (a.slot_tiles * NB);
+  __shared__ f32x4 lds_o[SPLIT == 1 ? 1 : 4][64];
+  __shared__ float2 lds_ml[SPLIT == 1 ? 1 : 4][64];
+  const int per_wg = a.slot_tiles * NB * SPLIT;
+  const int wg = blockIdx.x / per_wg;
   const Desc d = reinterpret_cast<const Desc*>(a.desc)[wg];
   if (d.parts == 0) return;
-  const int piece = (blockIdx.x % (a.slot_tiles * NB)) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int piece = SPLIT == 1 ? (blockIdx.x % per_wg) * 4 + wave : blockIdx.x % per_wg;
   const int wq = piece / (NB * 4), x = piece % (NB * 4);
   const int row = wq * kTile + (lane & 31);
   if (wq * kTile >= d.rows) return;
+  const int each = SPLIT == 1 ? d.parts : ceil_div(d.parts, SPLIT);
+  const int k_first = SPLIT == 1 ? 0 : wave * each, k_end = min(d.parts, k_first + each);
   float m = neg_inf(), l = 0.f;
   f32x4 o{0.f, 0.f, 0.f, 0.f};
+  auto add = [&](float2 ml, f32x4 y) {
+    const float top = fmaxf(m, ml.x), ref = top == neg_inf() ? 0.f : top;
+    const float sa = __builtin_amdgcn_exp2f(m - ref), sb = __builtin_amdgcn_exp2f(ml.x - ref);
+    m = top;
+    l = l * sa + ml.y * sb;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) o[z] = o[z] * sa + y[z] * sb;
+  };
   // four parts' loads at a time: the loop is a chain of latencies otherwise
   constexpr int kBatch = 4;
 #pragma unroll 1
-  for (int k0 = 0; k0 < d.parts; k0 += kBatch) {
+  for (int k0 = k_first; k0 < k_end; k0 += kBatch) {
     float2 ml[kBatch];
     f32x4 y[kBatch];
 #pragma unroll
@@ -680,21 +682,22 @@ __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
       const int k = k0 + j;
       ml[j] = make_float2(neg_inf(), 0.f);
       y[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (k < d.parts) {
+      if (k < k_end && row < d.rows) {
         const int64_t slot = (static_cast<int64_t>(wg + k) * 2 + (k == 0 ? 1 : 0)) * a.slot_tiles + wq;
         ml[j] = a.ml[slot * kTile + (lane & 31)];
         y[j] = reinterpret_cast<const f32x4*>(a.part)[slot * (NB * 4 * 64) + x * 64 + lane];
       }
     }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const float top = fmaxf(m, ml[j].x), ref = top == neg_inf() ? 0.f : top;
-      const float sa = __builtin_amdgcn_exp2f(m - ref), sb = __builtin_amdgcn_exp2f(ml[j].x - ref);
-      m = top;
-      l = l * sa + ml[j].y * sb;
+    for (int j = 0; j < kBatch; ++j) add(ml[j], y[j]);
+  }
+  if constexpr (SPLIT > 1) {
+    lds_ml[wave][lane] = make_float2(m, l);
+    lds_o[wave][lane] = o;
+    __syncthreads();
+    if (wave != 0) return;
 #pragma unroll
-      for (int z = 0; z < 4; ++z) o[z] = o[z] * sa + y[j][z] * sb;
-    }
+    for (int k = 1; k < SPLIT; ++k) add(lds_ml[k][lane], lds_o[k][lane]);
   }
   if (row >= d.rows) return;
   const int i = (d.m0 + row) / a.G, g = (d.m0 + row) - i * a.G;
@@ -705,51 +708,73 @@ __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
   if (a.lse && x == 0 && lane < 32) a.lse[out_at] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
 }
 
-// Work groups of the first launch: one per compute unit (the registers allow
-// no second).
-constexpr int kMaxGrid = 512;
-int grid_of() {
-  const int n = compute_units();
-  return n < kMaxGrid ? n : kMaxGrid;
+constexpr int kMaxGrid = 1024;
+
+// Waves of a work group.  A request's rows are at most this many tiles of 32;
+// a work group of 4 waves has half the startup and joining of one of 8, and
+// two of them on a compute unit overlap it; 8 waves cut the work half as
+// often and hold more rows.
+int waves_of(int gamma, int G, int D) {
+  return D == 256 || static_cast<int64_t>(gamma + 1) * G <= kTile ? 4 : 8;
 }
 
 int slot_tiles_of(int gamma, int Hq, int Hkv, int D) {
-  const int W = D == 256 ? 4 : 8;
+  const int W = waves_of(gamma, Hq / Hkv, D);
   const int64_t rows = static_cast<int64_t>(gamma + 1) * (Hq / Hkv);
   return rows >= W * kTile ? W : ceil_div(rows, kTile);
 }
 
-template <int FMT, int D>
+// Work groups: as many as the device holds at once.
+int grid_of(int gamma, int G, int D) {
+  const int per_unit = D != 256 && waves_of(gamma, G, D) == 4 ? 2 : 1;
+  const int n = compute_units() * per_unit, most = kMaxGrid / 2 * per_unit;
+  return n < most ? n : most;
+}
+
+template <int FMT, int D, int W>
 hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
-  constexpr int W = Shape<D>::kWaves, NB = D / 32;
-  const int G = a.G = a.Hq / a.Hkv;
+  constexpr int NB = D / 32;
   a.page_bytes = a.Hkv * PageLayout<FMT, D>::head_bytes(a.P);
-  a.blocks = ceil_div(static_cast<int64_t>(a.gamma + 1) * G, W * kTile);
+  a.blocks = ceil_div(static_cast<int64_t>(a.gamma + 1) * a.G, W * kTile);
   a.slot_tiles = slot_tiles_of(a.gamma, a.Hq, a.Hkv, D);
   a.min_units = W;  // a power of two, and no less than a tile's weight
-  const int grid = grid_of();
+  const int grid = grid_of(a.gamma, a.G, D);
   char* p = static_cast<char*>(ws);
   a.desc = reinterpret_cast<int32_t*>(p);
   a.ml = reinterpret_cast<float2*>(p + kMaxGrid * sizeof(Desc));
   a.part = reinterpret_cast<float*>(p + kMaxGrid * sizeof(Desc) +
-                                    static_cast<size_t>(kMaxGrid) * 2 * a.slot_tiles * kTile * sizeof(float2));
-  cache_attention_tiles<FMT, D><<<grid, W * 64, 0, s>>>(a);
+                                    static_cast<size_t>(grid) * 2 * a.slot_tiles * kTile * sizeof(float2));
+  cache_attention_tiles<FMT, D, W><<<grid, W * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  cache_attention_join<FMT, D><<<grid * a.slot_tiles * NB, 256, 0, s>>>(a);
+  // few heads and requests: many parts each
+  const bool many = static_cast<int64_t>(a.R) * a.blocks * a.Hkv * 4 <= grid;
+  if (many) cache_attention_join<D, 4><<<grid * a.slot_tiles * NB * 4, 256, 0, s>>>(a);
+  else cache_attention_join<D, 1><<<grid * a.slot_tiles * NB, 256, 0, s>>>(a);
   return hipGetLastError();
+}
+
+template <int FMT, int D>
+hipError_t run_w(AttnArgs& a, void* ws, hipStream_t s) {
+  if constexpr (D != 256) {
+    if (waves_of(a.gamma, a.G, D) == 8) return run<FMT, D, 8>(a, ws, s);
+  }
+  return run<FMT, D, 4>(a, ws, s);
 }
 
 template <int FMT>
 hipError_t run_d(int D, AttnArgs& a, void* ws, hipStream_t s) {
-  return D == 64 ? run<FMT, 64>(a, ws, s) : D == 128 ? run<FMT, 128>(a, ws, s) : run<FMT, 256>(a, ws, s);
+  return D == 64 ? run_w<FMT, 64>(a, ws, s) : D == 128 ? run_w<FMT, 128>(a, ws, s) : run_w<FMT, 256>(a, ws, s);
 }
 
 }  // namespace
 
 size_t cache_attention_workspace_bytes(int R, int gamma, int Hq, int Hkv, int D) {
   (void)R;
-  const size_t rows = static_cast<size_t>(kMaxGrid) * 2 * slot_tiles_of(gamma, Hq, Hkv, D) * kTile;
+  // sized for the largest grid: the size does not depend on the device
+  const int W = waves_of(gamma, Hq / Hkv, D);
+  const size_t grid = D != 256 && W == 4 ? kMaxGrid : kMaxGrid / 2;
+  const size_t rows = grid * 2 * slot_tiles_of(gamma, Hq, Hkv, D) * kTile;
   return kMaxGrid * sizeof(Desc) + rows * (sizeof(float2) + static_cast<size_t>(D) * sizeof(float));
 }
 
@@ -758,7 +783,7 @@ hipError_t cache_attention_launch(int fmt, int R, int gamma, int Hq, int Hkv, in
                                   const int32_t* row0, const int32_t* ell, const int32_t* len, const int32_t* table,
                                   const void* pool, void* out, float* lse, void* ws, hipStream_t s) {
   AttnArgs a{};
-  a.R = R, a.gamma = gamma, a.Hq = Hq, a.Hkv = Hkv, a.P = P, a.n_pages = n_pages, a.max_pages = max_pages;
+  a.R = R, a.gamma = gamma, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.P = P, a.n_pages = n_pages, a.max_pages = max_pages;
   a.q = static_cast<const uint16_t*>(q);
   a.scale_log2 = scale == 0.f ? 1.f : (scale < 0.f ? -scale : scale) * kLog2e;
   a.q_keep = scale == 0.f ? 0u : 0xFFFFFFFFu;
