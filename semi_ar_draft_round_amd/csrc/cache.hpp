@@ -81,17 +81,12 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale) {
   return r.u;
 }
 
-// The scale 2^(b - 127) of a K scale byte; 255 gives NaN.  Quantisation writes 1 .. 254 or 255; byte 0
-// (2^-127) is a subnormal.
-__device__ __forceinline__ float k_scale_value(uint32_t b) {
-  return __uint_as_float(b == 255u ? 0x7FC00000u : b == 0u ? 0x00400000u : b << 23);
-}
-
-// Vector of 8 bf16 values of 8 codes; a NaN scale gives NaNs.
+// Eight codes times the scale of a K scale byte b: 2^(b - 127), or NaN for
+// 255.  The conversion reads the scale's exponent field as such a byte: 255
+// gives NaN for every code, 0 gives 2^-127 (both checked on the device).
+__device__ __forceinline__ float k_scale_value(uint32_t b) { return __uint_as_float(b << 23); }
 __device__ __forceinline__ u32x4 fp4_octet(uint32_t w, float scale) {
-  u32x4 r{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale), fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)};
-  if (scale != scale) r = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
-  return r;
+  return u32x4{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale), fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)};
 }
 
 }  // namespace dspark

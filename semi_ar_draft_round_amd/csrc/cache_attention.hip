@@ -36,6 +36,7 @@ struct AttnArgs {
   int blocks;              // row blocks a request can have
   int min_units;           // the least units worth a work group
   int slot_tiles;          // row tiles of a workspace slot
+  int row_shift;           // log2 of the row tiles that cost no more than one
   const uint16_t* q;
   float scale_log2;        // |scale| log2(e) (1 for a zero scale, with q masked to zero)
   uint32_t q_keep, q_flip; // q & keep ^ flip: the scale's sign, or zero
@@ -86,7 +87,7 @@ struct Block {
   int m0, rows;
   int len;               // the first new token, at most kFar
   int head, first, count;
-  int shift;             // log2 of the waves along the rows (1, 2, 4, 8)
+  int shift;             // log2 of a tile's weight: what halves the waves along the tokens
 };
 constexpr int kFar = 1 << 29;  // past every table (2^20 pages of 128 tokens)
 
@@ -101,7 +102,7 @@ __device__ __forceinline__ Block block_of(const AttnArgs& a, int entry, int rows
     return b;
   }
   const int qt = (b.rows + kTile - 1) / kTile;
-  b.shift = qt == 1 ? 0 : 32 - __clz(qt - 1);
+  b.shift = max(0, (qt == 1 ? 0 : 32 - __clz(qt - 1)) - a.row_shift);
   const int cap = a.max_pages * a.P;
   const int end = min(b.len + (b.m0 + b.rows - 1) / a.G + 1, cap);
   const int tiles = (end + kTile - 1) / kTile;
@@ -119,30 +120,46 @@ __device__ __forceinline__ Block block_of(const AttnArgs& a, int entry, int rows
   return b;
 }
 
+// The same in every lane, so in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ Block uniform(const Block& b) {
+  return Block{uniform(b.m0),   uniform(b.rows),  uniform(b.len),  uniform(b.head),
+               uniform(b.first), uniform(b.count), uniform(b.shift)};
+}
+
 // The token that K row slot p (0 .. 15) of a 16-token block holds: with this
 // order the accumulators of half h are tokens 8 h .. 8 h + 7 in turn.
 __device__ __forceinline__ int token_of_slot(int p) { return ((p >> 2) & 1) * 8 + (p >> 3) * 4 + (p & 3); }
-
-// The operands of one tile, loaded ahead of their use.  K: this lane's row
-// (token slot lane % 32 of the tile), the 8 dims of its half at every step.
-// V: this lane's dim (lane % 32 of every block of 32), the 8 tokens of its
-// half of each 16.
-template <int FMT, int D>
-struct KTile;
-template <int FMT, int D>
-struct VTile;
 
 // Keeps a rare branch a branch: without it the compiler turns the few
 // instructions inside into selects that every tile pays for.
 __device__ __forceinline__ void rare() { asm volatile(""); }
 
+// Loads before this stay before those after it: they return in the order of
+// their use (the scheduler likes to reverse them, and the first product then
+// waits for the last load).  Everything but vector memory may cross.
+__device__ __forceinline__ void keep_load_order() { __builtin_amdgcn_sched_barrier(0x78F); }
+
+// The operands of one tile, loaded ahead of their use.  K: this lane's row
+// (token slot lane % 32 of the tile), the 8 dims of its half at every step.
+// V: this lane's dim (lane % 32 of every block of 32), the 8 tokens of its
+// half of each 16.  Addresses are a wave's base (the page's part for the head
+// and the token in it, in scalar registers) and a lane's constant offset.
+template <int FMT, int D>
+struct KTile;
+template <int FMT, int D>
+struct VTile;
+
 template <int D>
 struct KTile<DSPARK_CACHE_BF16, D> {
   u32x4 x[D / 16];
-  __device__ __forceinline__ void load(const char* head, int P, int t, int h) {
-    const char* p = head + PageLayout<DSPARK_CACHE_BF16, D>::k(P, t, h);
+  static __device__ __forceinline__ uint32_t lane_offset(int slot, int h) {
+    return (slot >> 4) * (32 * D) + (h * 16 + token_of_slot(slot & 15)) * 16;
+  }
+  __device__ __forceinline__ void load(const char* head, int, int t, uint32_t lane, int) {
+    const char* p = head + static_cast<int64_t>(t >> 4) * (32 * D);
 #pragma unroll
-    for (int u = 0; u < D / 16; ++u) x[u] = *reinterpret_cast<const u32x4*>(p + u * 512);
+    for (int u = 0; u < D / 16; ++u) x[u] = *reinterpret_cast<const u32x4*>(p + u * 512 + lane);
   }
   static __device__ __forceinline__ int q_dim(int u, int h) { return 16 * u + 8 * h; }
   template <typename Q>
@@ -162,12 +179,15 @@ struct KTile<DSPARK_CACHE_FP4, D> {
   static constexpr int E = D / 32;
   u32x4 x[D / 64];
   uint32_t sc[(E + 3) / 4];
-  __device__ __forceinline__ void load(const char* head, int P, int t, int h) {
-    typedef PageLayout<DSPARK_CACHE_FP4, D> L;
-    const char* p = head + L::k(P, t, h);
+  static __device__ __forceinline__ uint32_t lane_offset(int slot, int h) {
+    return (slot >> 4) * (8 * D) + (h * 16 + token_of_slot(slot & 15)) * 16;
+  }
+  // token: the lane's token counted from t
+  __device__ __forceinline__ void load(const char* head, int P, int t, uint32_t lane, int token) {
+    const char* p = head + static_cast<int64_t>(t >> 4) * (8 * D);
 #pragma unroll
-    for (int g = 0; g < D / 64; ++g) x[g] = *reinterpret_cast<const u32x4*>(p + g * 512);
-    const char* b = head + L::k_scale(P, t);
+    for (int g = 0; g < D / 64; ++g) x[g] = *reinterpret_cast<const u32x4*>(p + g * 512 + lane);
+    const char* b = head + P * (D / 2) + t * E + static_cast<uint32_t>(token * E);
     if constexpr (E == 2) {
       sc[0] = *reinterpret_cast<const uint16_t*>(b);
     } else {
@@ -179,27 +199,13 @@ struct KTile<DSPARK_CACHE_FP4, D> {
   template <typename Q>
   __device__ __forceinline__ f32x16 scores(const Q& q, int h) const {
     f32x16 s = {0.f};
-    bool bad = false;
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
-      const uint32_t b = (sc[g / 2] >> (16 * (g & 1) + 8 * h)) & 0xFFu;
-      bad |= b == 255u;
-      const float scale = __uint_as_float(b << 23);
+      const float scale = k_scale_value((sc[g / 2] >> (16 * (g & 1) + 8 * h)) & 0xFFu);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint32_t w = x[g][v];
-        const u32x4 k{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale), fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)};
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(k), as_bf16(q(4 * g + v)), s, 0, 0, 0);
-      }
-    }
-    // a NaN scale makes its token's scores NaN: slot r is accumulator j of half h with 8 (j / 4) + 4 h + j % 4 = r
-    const unsigned long long rows = __ballot(bad);
-    if (rows) {
-      rare();
-      const uint32_t r = static_cast<uint32_t>(rows) | static_cast<uint32_t>(rows >> 32);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if ((r >> (8 * (j / 4) + 4 * h + j % 4)) & 1u) s[j] = __builtin_nanf("");
+      for (int v = 0; v < 4; ++v)
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(fp4_octet(x[g][v], scale)), as_bf16(q(4 * g + v)), s, 0, 0,
+                                                    0);
     }
     return s;
   }
@@ -208,10 +214,15 @@ struct KTile<DSPARK_CACHE_FP4, D> {
 template <int D>
 struct VTile<DSPARK_CACHE_BF16, D> {
   u32x4 x[2][D / 32];
-  __device__ __forceinline__ void load(int s, const char* head, int P, int t16, int row, int h) {
-    const char* p = head + PageLayout<DSPARK_CACHE_BF16, D>::v(P, t16 + 8 * h, row);
+  static __device__ __forceinline__ uint32_t lane_offset(int row, int h) { return (h * D + row) * 16; }
+  // block s of the tile: 16 tokens from t of the page on
+  __device__ __forceinline__ void load(int s, const char* head, int P, int t, uint32_t lane, int) {
+    const char* p = head + 2 * P * D + static_cast<int64_t>(t >> 4) * (32 * D);
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) x[s][b] = *reinterpret_cast<const u32x4*>(p + b * 512);
+    for (int b = 0; b < D / 32; ++b) {
+      x[s][b] = *reinterpret_cast<const u32x4*>(p + b * 512 + lane);
+      keep_load_order();
+    }
   }
   __device__ __forceinline__ u32x4 operand(int s, int b) const { return x[s][b]; }
   __device__ __forceinline__ float weight(int, float p) const { return p; }
@@ -224,9 +235,9 @@ struct VTile<DSPARK_CACHE_FP4, D> {
   static constexpr int E = D / 32;
   uint32_t x[2][E];
   f32x4 sc[2][2];
-  __device__ __forceinline__ void load(int s, const char* head, int P, int t16, int row, int h) {
-    typedef PageLayout<DSPARK_CACHE_FP4, D> L;
-    const char* p = head + L::v(P, t16 + 8 * h, row);
+  static __device__ __forceinline__ uint32_t lane_offset(int row, int h) { return (h * 32 + row) * (4 * E); }
+  __device__ __forceinline__ void load(int s, const char* head, int P, int t, uint32_t lane, int h) {
+    const char* p = head + P * (D / 2 + E) + static_cast<int64_t>(t >> 4) * (8 * D) + lane;
     if constexpr (E == 2) {
       const u32x2 w = *reinterpret_cast<const u32x2*>(p);
       x[s][0] = w[0], x[s][1] = w[1];
@@ -238,14 +249,11 @@ struct VTile<DSPARK_CACHE_FP4, D> {
         for (int j = 0; j < 4; ++j) x[s][4 * i + j] = w[j];
       }
     }
-    const f32x4* b = reinterpret_cast<const f32x4*>(head + L::v_scale(P, t16 + 8 * h));
+    const f32x4* b = reinterpret_cast<const f32x4*>(head + P * (D + E) + t * 4 + static_cast<uint32_t>(h * 32));
     sc[s][0] = b[0];
     sc[s][1] = b[1];
   }
-  __device__ __forceinline__ u32x4 operand(int s, int b) const {
-    const uint32_t w = x[s][b];
-    return u32x4{fp4_pair<0>(w, 1.f), fp4_pair<1>(w, 1.f), fp4_pair<2>(w, 1.f), fp4_pair<3>(w, 1.f)};
-  }
+  __device__ __forceinline__ u32x4 operand(int s, int b) const { return fp4_octet(x[s][b], 1.f); }
   __device__ __forceinline__ float weight(int j, float p) const { return p * sc[j / 8][(j % 8) / 4][j % 4]; }
   // a hidden token's scale may be anything, its weight is zero
   __device__ __forceinline__ void hide(int j, bool see) {
@@ -306,9 +314,29 @@ struct Deal {
   }
 };
 
+// Whether a work group's waves share their tiles through LDS.
+constexpr bool shared_tiles(int fmt, int W) { return fmt == DSPARK_CACHE_BF16 && W == 8; }
+
+// Moves a wave's 64 x 16 bytes from memory to LDS at byte `to`, lane by lane,
+// past the registers.  Counts as an outstanding vector load; the compiler
+// does not know of it, so its waits may be longer than they need to be, never
+// shorter, and the reader's wait is written out below.
+__device__ __forceinline__ void copy_to_lds(const char* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+
+// Outstanding vector loads down to N, LDS reads down to none, then the work
+// group's barrier: what every wave waited for is there for all, and what
+// every wave read may be overwritten.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // W waves: 256 registers a wave for heads of 64 and 128 dims, so 8 waves a
 // compute unit, as one work group or two; 512 and 4 waves for 256 dims.
-template <int FMT, int D, int W>
+// TWO: pages of 16 tokens, two a tile.
+template <int FMT, int D, int W, bool TWO>
 __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tiles(AttnArgs a) {
   typedef PageLayout<FMT, D> L;
   constexpr int T = W * 64, NB = D / 32, KS = D / 16;
@@ -316,6 +344,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   // heads of 256 dims: the output alone takes 128 registers and a tile 128,
   // so the query rows go to LDS
   constexpr bool kQueryInLds = D == 256;
+  constexpr bool kShared = shared_tiles(FMT, W);
+  constexpr int kAlong = kShared ? 4 : W;
   // (the wave's own, under its output, which it writes when done with them)
   __shared__ f32x4 lds_own[W][NB * 4][64];
   __shared__ float2 lds_ml[W][64];
@@ -387,7 +417,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 
 #pragma unroll 1
   for (int64_t u = u0; u < u1;) {
-    const Block b = block_of(a, entry, rows_max);
+    const Block b = uniform(block_of(a, entry, rows_max));
     const int64_t per_head = static_cast<int64_t>(b.count) << b.shift;
     if (u >= base + per_head * a.Hkv) {
       base += per_head * a.Hkv;
@@ -395,17 +425,17 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       continue;
     }
     const int r = entry / a.blocks;
-    const int hk = static_cast<int>(quotient(u - base, per_head));
+    const int hk = uniform(static_cast<int>(quotient(u - base, per_head)));
     const int64_t seg = base + hk * per_head, seg_end = seg + per_head;
     // the tiles whose first unit is in this run
     const int weight = 1 << b.shift;
-    const int t0 = static_cast<int>((u - seg + weight - 1) >> b.shift);
-    const int t1 = u1 < seg_end ? static_cast<int>((u1 - seg + weight - 1) >> b.shift) : b.count;
+    const int t0 = uniform(static_cast<int>((u - seg + weight - 1) >> b.shift));
+    const int t1 = uniform(u1 < seg_end ? static_cast<int>((u1 - seg + weight - 1) >> b.shift) : b.count);
     u = seg_end;
     if (t0 >= t1) continue;
     const int qt = ceil_div(b.rows, kTile);
-    const int WT = W >> b.shift;  // waves along the tokens
-    const int wq = wave % qt, wt = wave / qt;
+    const int WT = kAlong >> b.shift;  // waves along the tokens
+    const int wt = uniform(wave / qt), wq = wave - wt * qt;
     const bool active = wt < WT;
 
     // this lane's query row
@@ -424,157 +454,259 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
     Acc<D> acc;
     acc.m = neg_inf();
     acc.l = 0.f;
+    float minus_ref = 0.f;  // -m, or 0 while nothing was seen
 #pragma unroll
     for (int x = 0; x < NB; ++x) acc.o[x] = f32x16{0.f};
 
-    const int steps = active && t0 + wt < t1 ? (t1 - t0 - wt + WT - 1) >> (__ffs(WT) - 1) : 0;
-    if (steps > 0) {
-      // the query rows' operands: in registers, or the wave's own slice of LDS
-      u32x4 q_reg[kQueryInLds ? 1 : KS];
+    const int tiles = t1 - t0;
+    const char* pool = a.pool + hk * L::head_bytes(a.P);
+    const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
+    const int lp = TWO ? 4 : 31 - __clz(a.P);
+    // tile t of the run: its first token
+    auto token_at = [&](int t) {
+      const int x = t0 + t;
+      return (x < b.head ? x : x - b.head + b.first) * kTile;
+    };
+    // page ids of tiles t, t + WT, .. for 64 of them, a tile a lane (two pages
+    // a tile when P is 16): -1 where the table has none
+    struct Ids {
+      int v0, v1;
+    };
+    auto fetch_ids = [&](int t) {
+      const int tok = token_at(min(t + lane * WT, tiles - 1));
+      const int s0 = tok >> lp, s1 = (tok + 16) >> lp;
+      Ids x;
+      x.v0 = s0 < a.max_pages ? page_or_none(table[s0], a.n_pages) : -1;
+      x.v1 = !TWO ? x.v0 : s1 < a.max_pages ? page_or_none(table[s1], a.n_pages) : -1;
+      return x;
+    };
+    // which of those tiles need no mask
+    auto clear_of = [&](const Ids& x, int t) {
+      const int tok = token_at(min(t + lane * WT, tiles - 1));
+      return __ballot(x.v0 >= 0 && x.v1 >= 0 && tok + kTile - 1 <= pos_a && (tok >= low_b || tok + kTile <= a.sinks));
+    };
+    // the part for this head of a page; a missing page is read as page 0 and masked
+    auto head_of = [&](int id) { return pool + max(id, 0) * a.page_bytes; };
+    // a lane's offsets from its wave's bases; with two pages a tile the key
+    // rows of the upper 16 tokens lie in the other one
+    const uint32_t k_lane = KTile<FMT, D>::lane_offset(TWO ? col & 15 : col, h);
+    const uint32_t v_lane = VTile<FMT, D>::lane_offset(col, h);
+
+    // the query rows' operands: in registers, or the wave's own slice of LDS
+    u32x4 q_reg[kQueryInLds ? 1 : KS];
 #pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        u32x4 v = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
+    for (int x = 0; x < KS; ++x) {
+      u32x4 v = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
 #pragma unroll
-        for (int y = 0; y < 4; ++y) v[y] = (v[y] & a.q_keep) ^ a.q_flip;
-        if constexpr (kQueryInLds) lds_own[wave][x][lane] = __builtin_bit_cast(f32x4, v);
-        else q_reg[x] = v;
+      for (int y = 0; y < 4; ++y) v[y] = (v[y] & a.q_keep) ^ a.q_flip;
+      if constexpr (kQueryInLds) lds_own[wave][x][lane] = __builtin_bit_cast(f32x4, v);
+      else q_reg[x] = v;
+    }
+    auto q = [&](int x) {
+      if constexpr (kQueryInLds) return __builtin_bit_cast(u32x4, lds_own[wave][x][lane]);
+      else return q_reg[x];
+    };
+
+    // One tile: its scores s, its values, first token ct and pages c0, c1.
+    auto absorb = [&](f32x16 s, VTile<FMT, D>& vt, int ct, int c0, int c1, bool clear) {
+      if (!clear) {
+        rare();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int t = ct + 16 * (j / 8) + 8 * h + j % 8;
+          const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
+          s[j] = see ? s[j] : neg_inf();
+          vt.hide(j, see);
+        }
       }
-      auto q = [&](int x) {
-        if constexpr (kQueryInLds) return __builtin_bit_cast(u32x4, lds_own[wave][x][lane]);
-        else return q_reg[x];
-      };
-      const char* pool = a.pool + hk * L::head_bytes(a.P);
-      const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
-      const int lp = 31 - __clz(a.P);
-      // page ids of the wave's next 64 tiles, a tile a lane (two pages a tile
-      // when P is 16), and which of those tiles need no mask
-      int id0_v = -1, id1_v = -1;
+      float top = s[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
+      top = fmaxf(top, xor32(top)) * a.scale_log2;
+      // weights are relative to acc.m, which follows the maximum once that is 2^8 ahead
+      if (__any(top > acc.m + kSlack)) {
+        const float m = fmaxf(acc.m, top);
+        const float keep = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(acc.m - m);
+        acc.l *= keep;
+        acc.m = m;
+        minus_ref = m == neg_inf() ? 0.f : -m;
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc.o[x][j] *= keep;
+      }
+      float p[16], sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, minus_ref));
+        sum += p[j];
+      }
+      acc.l += sum;
+      u32x4 pk[2];
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) pk[j / 8][(j % 8) / 2] = bf16_pair(vt.weight(j, p[j]), vt.weight(j + 1, p[j + 1]));
+      bool odd = false;
+      if constexpr (FMT == DSPARK_CACHE_BF16) {
+        if (!clear) {
+          // tokens that no row of the wave sees become zeros; of the others, values that are not finite too
+          rare();
+#pragma unroll
+          for (int s2 = 0; s2 < 2; ++s2) {
+            u32x4 keep{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int t = ct + 16 * s2 + 8 * h + e;
+              const bool see = (s2 ? c1 : c0) >= 0 && t <= pos_b && (t >= low_a || t < a.sinks);
+              keep[e / 2] |= see ? 0xFFFFu << (16 * (e & 1)) : 0u;
+            }
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                uint32_t v = vt.x[s2][x][w] & keep[w];
+                if ((v & 0x7F80u) == 0x7F80u) odd = true, v &= 0xFFFF0000u;
+                if ((v & 0x7F800000u) == 0x7F800000u) odd = true, v &= 0x0000FFFFu;
+                vt.x[s2][x][w] = v;
+              }
+          }
+        }
+      }
+#pragma unroll
+      for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+          acc.o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vt.operand(s2, x)), as_bf16(pk[s2]), acc.o[x], 0,
+                                                             0, 0);
+      if constexpr (FMT == DSPARK_CACHE_BF16)
+        if (__any(odd)) {
+          uint32_t visible = 0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int t = ct + 16 * (j / 8) + 8 * h + j % 8;
+            const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
+            visible |= static_cast<uint32_t>(see) << j;
+          }
+          add_non_finite<D>(acc.o, p, visible, head_of(c0), head_of(c1), a.P, ct & (a.P - 1), (ct + 16) & (a.P - 1), lane);
+        }
+    };
+
+    if constexpr (kShared) {
+      // Rounds of WT tiles through a ring of 8 tiles in LDS.  A wave copies
+      // an eighth of every round, whole 1 KB operands in the order the lanes
+      // read them, and multiplies its own tile of it.  Copies are issued
+      // 8 / WT - 1 rounds ahead, past the run's end too (its last tile
+      // again), so that what is outstanding is known.
+      constexpr int F = D / 8;  // operands of a tile: D / 16 of K, as many of V
+      static_assert(sizeof(lds_own) == 8 * F * 1024, "the ring lies under the outputs");
+      const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+          (__attribute__((address_space(3))) char*)(&lds_own[0][0][0])));
+      const int depth = 8 / WT, lw = __ffs(WT) - 1;
+      const int rounds = (tiles + WT - 1) >> lw;
+      const int n = F * WT / 8;                   // operands a wave copies in a round
+      const int mine = wave * n / F, f0 = wave * n - mine * F;
+      const bool keys = f0 < KS;                  // all of them K, or all V
+      Ids from{-1, -1}, own{-1, -1};
       unsigned long long clear_v = 0;
-      auto tile_at = [&](int k) {
-        const int t = t0 + wt + k * WT;
-        return t < b.head ? t : t - b.head + b.first;
+      auto copy = [&](int round) {
+        if ((round & 63) == 0) {
+          rare();
+          from = fetch_ids((round << lw) + mine);
+        }
+        const int tok = token_at(min((round << lw) + mine, tiles - 1));
+        const char* p0 = head_of(__builtin_amdgcn_readlane(from.v0, round & 63));
+        const char* p1 = TWO ? head_of(__builtin_amdgcn_readlane(from.v1, round & 63)) : p0;
+        const int t = TWO ? 0 : (tok & (a.P - 1)) >> 4;
+        uint32_t to = ring + ((((round & (depth - 1)) << lw) + mine) * F + f0) * 1024;
+        if (keys) {
+          const char* p = (TWO && col >= 16 ? p1 : p0) + t * (32 * D) + f0 * 512 + k_lane;
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) copy_to_lds(p + j * 512, to + j * 1024);
+        } else {
+          const int g = f0 - KS;
+          const int64_t v0 = 2 * a.P * D + t * (32 * D) + v_lane;
+#pragma unroll 1
+          for (int j = g; j < g + n; ++j) {
+            const int s2 = j / NB;
+            copy_to_lds((TWO && s2 ? p1 : p0 + (TWO ? 0 : s2 * (32 * D))) + v0 + (j - s2 * NB) * 512, to);
+            to += 1024;
+          }
+        }
       };
-      auto fetch_ids = [&](int k0) {
-        const int k = min(k0 + lane, steps - 1), tok = tile_at(k) * kTile;
-        const int s0 = tok >> lp, s1 = (tok + 16) >> lp;
-        id0_v = s0 < a.max_pages ? page_or_none(table[s0], a.n_pages) : -1;
-        id1_v = s1 < a.max_pages ? page_or_none(table[s1], a.n_pages) : -1;
-        clear_v = __ballot(id0_v >= 0 && id1_v >= 0 && tok + kTile - 1 <= pos_a &&
-                           (tok >= low_b || tok + kTile <= a.sinks));
-      };
+      for (int round = 0; round < depth - 1; ++round) copy(round);
+#pragma unroll 1
+      for (int round = 0; round < rounds; ++round) {
+        // this round's copies are there: those of the depth - 2 after it may be on their way
+        if (WT == 4) wait_and_meet<0>();
+        else if (WT == 2) wait_and_meet<2 * F / 4>();
+        else wait_and_meet<6 * F / 8>();
+        copy(round + depth - 1);
+        if ((round & 63) == 0) {
+          rare();
+          own = fetch_ids((round << lw) + wt);
+          clear_v = clear_of(own, (round << lw) + wt);
+        }
+        const int t = (round << lw) + wt;
+        if (active && t < tiles) {
+          const u32x4* tile = reinterpret_cast<const u32x4*>(&lds_own[0][0][0]) +
+                              (((round & (depth - 1)) << lw) + wt) * (F * 64) + lane;
+          KTile<FMT, D> kt;
+          VTile<FMT, D> vt;
+#pragma unroll
+          for (int u = 0; u < KS; ++u) kt.x[u] = tile[u * 64];
+          const f32x16 s = kt.scores(q, h);
+#pragma unroll
+          for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+            for (int x = 0; x < NB; ++x) vt.x[s2][x] = tile[(KS + s2 * NB + x) * 64];
+          const int c0 = __builtin_amdgcn_readlane(own.v0, round & 63);
+          const int c1 = TWO ? __builtin_amdgcn_readlane(own.v1, round & 63) : c0;
+          absorb(s, vt, token_at(t), c0, c1, (clear_v >> (round & 63)) & 1u);
+        }
+      }
+      wait_and_meet<0>();
+    } else if (active && wt < tiles) {
+      // Every wave for itself, straight into registers, a tile ahead.
+      const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
+      const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
       KTile<FMT, D> kt;
       VTile<FMT, D> vt;
-      // the tile in flight; a missing page is read as page 0 and masked
+      Ids ids{-1, -1};
+      unsigned long long clear_v = 0;
       int id0 = 0, id1 = 0, tok = 0;
-      const char *head0 = nullptr, *head1 = nullptr;
+      auto fetch = [&](int k) {
+        ids = fetch_ids(wt + k * WT);
+        clear_v = clear_of(ids, wt + k * WT);
+      };
       auto aim = [&](int k) {
-        id0 = __builtin_amdgcn_readlane(id0_v, k & 63);
-        id1 = __builtin_amdgcn_readlane(id1_v, k & 63);
-        tok = tile_at(k) * kTile;
-        head0 = pool + max(id0, 0) * a.page_bytes;
-        head1 = pool + max(id1, 0) * a.page_bytes;
+        id0 = __builtin_amdgcn_readlane(ids.v0, k & 63);
+        id1 = TWO ? __builtin_amdgcn_readlane(ids.v1, k & 63) : id0;
+        tok = token_at(wt + k * WT);
       };
       auto load_k = [&]() {
-        kt.load(col < 16 ? head0 : head1, a.P, ((tok + (col & 16)) & (a.P - 1)) + token_of_slot(col & 15), h);
+        kt.load(head_of(TWO && col >= 16 ? id1 : id0), TWO ? 16 : a.P, TWO ? 0 : tok & (a.P - 1), k_lane, k_token);
       };
       auto load_v = [&]() {
-        vt.load(0, head0, a.P, tok & (a.P - 1), col, h);
-        vt.load(1, head1, a.P, (tok + 16) & (a.P - 1), col, h);
+        const int t = TWO ? 0 : tok & (a.P - 1);
+        vt.load(0, head_of(id0), TWO ? 16 : a.P, t, v_lane, h);
+        vt.load(1, head_of(id1), TWO ? 16 : a.P, TWO ? 0 : t + 16, v_lane, h);
       };
-      fetch_ids(0);
+      fetch(0);
       aim(0);
       load_k();
       load_v();
 #pragma unroll 1
       for (int k = 0; k < steps; ++k) {
-        f32x16 s = kt.scores(q, h);
-        const bool clear = (clear_v >> (k & 63)) & 1u;
+        const f32x16 s = kt.scores(q, h);
         const int c0 = id0, c1 = id1, ct = tok;
-        const char *ch0 = head0, *ch1 = head1;
+        const bool clear = (clear_v >> (k & 63)) & 1u;
         // the next tile's keys (after the last tile: its own again, unused)
-        const int next = min(k + 1, steps - 1);
-        if ((k & 63) == 63) fetch_ids(next);
-        aim(next);
-        load_k();
-        if (!clear) {
+        if ((k & 63) == 63 && k + 1 < steps) {
           rare();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int t = ct + 16 * (j / 8) + 8 * h + j % 8;
-            const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
-            s[j] = see ? s[j] : neg_inf();
-            vt.hide(j, see);
-          }
+          fetch(k + 1);
         }
-        float top = s[0];
-#pragma unroll
-        for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
-        top = fmaxf(top, xor32(top)) * a.scale_log2;
-        // weights are relative to acc.m, which follows the maximum once that is 2^8 ahead
-        if (__any(top > acc.m + kSlack)) {
-          const float m = fmaxf(acc.m, top);
-          const float keep = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(acc.m - m);
-          acc.l *= keep;
-          acc.m = m;
-#pragma unroll
-          for (int x = 0; x < NB; ++x)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc.o[x][j] *= keep;
-        }
-        const float ref = acc.m == neg_inf() ? 0.f : acc.m;
-        float p[16], sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, -ref));
-          sum += p[j];
-        }
-        acc.l += sum;
-        u32x4 pk[2];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) pk[j / 8][(j % 8) / 2] = bf16_pair(vt.weight(j, p[j]), vt.weight(j + 1, p[j + 1]));
-        bool odd = false;
-        if constexpr (FMT == DSPARK_CACHE_BF16) {
-          if (!clear) {
-            // tokens that no row of the wave sees become zeros; of the others, values that are not finite too
-            rare();
-#pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2) {
-              u32x4 keep{0u, 0u, 0u, 0u};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int t = ct + 16 * s2 + 8 * h + e;
-                const bool see = (s2 ? c1 : c0) >= 0 && t <= pos_b && (t >= low_a || t < a.sinks);
-                keep[e / 2] |= see ? 0xFFFFu << (16 * (e & 1)) : 0u;
-              }
-#pragma unroll
-              for (int x = 0; x < NB; ++x)
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  uint32_t v = vt.x[s2][x][w] & keep[w];
-                  if ((v & 0x7F80u) == 0x7F80u) odd = true, v &= 0xFFFF0000u;
-                  if ((v & 0x7F800000u) == 0x7F800000u) odd = true, v &= 0x0000FFFFu;
-                  vt.x[s2][x][w] = v;
-                }
-            }
-          }
-        }
-#pragma unroll
-        for (int s2 = 0; s2 < 2; ++s2)
-#pragma unroll
-          for (int x = 0; x < NB; ++x)
-            acc.o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vt.operand(s2, x)), as_bf16(pk[s2]), acc.o[x], 0,
-                                                               0, 0);
-        if constexpr (FMT == DSPARK_CACHE_BF16)
-          if (__any(odd)) {
-            uint32_t visible = 0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int t = ct + 16 * (j / 8) + 8 * h + j % 8;
-              const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
-              visible |= static_cast<uint32_t>(see) << j;
-            }
-            add_non_finite<D>(acc.o, p, visible, ch0, ch1, a.P, ct & (a.P - 1), (ct + 16) & (a.P - 1), lane);
-          }
+        aim(min(k + 1, steps - 1));
+        load_k();
+        absorb(s, vt, ct, c0, c1, clear);
         load_v();
       }
     }
@@ -731,20 +863,21 @@ int grid_of(int gamma, int G, int D) {
   return n < most ? n : most;
 }
 
-template <int FMT, int D, int W>
+template <int FMT, int D, int W, bool TWO>
 hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
   constexpr int NB = D / 32;
   a.page_bytes = a.Hkv * PageLayout<FMT, D>::head_bytes(a.P);
   a.blocks = ceil_div(static_cast<int64_t>(a.gamma + 1) * a.G, W * kTile);
   a.slot_tiles = slot_tiles_of(a.gamma, a.Hq, a.Hkv, D);
-  a.min_units = W;  // a power of two, and no less than a tile's weight
+  a.min_units = W;  // no less than a tile's weight
+  a.row_shift = shared_tiles(FMT, W) ? 1 : 0;
   const int grid = grid_of(a.gamma, a.G, D);
   char* p = static_cast<char*>(ws);
   a.desc = reinterpret_cast<int32_t*>(p);
   a.ml = reinterpret_cast<float2*>(p + kMaxGrid * sizeof(Desc));
   a.part = reinterpret_cast<float*>(p + kMaxGrid * sizeof(Desc) +
                                     static_cast<size_t>(grid) * 2 * a.slot_tiles * kTile * sizeof(float2));
-  cache_attention_tiles<FMT, D, W><<<grid, W * 64, 0, s>>>(a);
+  cache_attention_tiles<FMT, D, W, TWO><<<grid, W * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // few heads and requests: many parts each
@@ -757,9 +890,10 @@ hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
 template <int FMT, int D>
 hipError_t run_w(AttnArgs& a, void* ws, hipStream_t s) {
   if constexpr (D != 256) {
-    if (waves_of(a.gamma, a.G, D) == 8) return run<FMT, D, 8>(a, ws, s);
+    if (waves_of(a.gamma, a.G, D) == 8)
+      return a.P == 16 ? run<FMT, D, 8, true>(a, ws, s) : run<FMT, D, 8, false>(a, ws, s);
   }
-  return run<FMT, D, 4>(a, ws, s);
+  return a.P == 16 ? run<FMT, D, 4, true>(a, ws, s) : run<FMT, D, 4, false>(a, ws, s);
 }
 
 template <int FMT>
