@@ -28,15 +28,14 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 32;       // tokens of a tile, and query rows of a wave
+constexpr int W = 4;            // waves of a work group
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
   int R, gamma, Hq, Hkv, G, P, n_pages, max_pages;
   int blocks;              // row blocks a request can have
-  int min_units;           // the least units worth a work group
   int slot_tiles;          // row tiles of a workspace slot
-  int row_shift;           // log2 of the row tiles that cost no more than one
   const uint16_t* q;
   float scale_log2;        // |scale| log2(e) (1 for a zero scale, with q masked to zero)
   uint32_t q_keep, q_flip; // q & keep ^ flip: the scale's sign, or zero
@@ -87,9 +86,17 @@ struct Block {
   int m0, rows;
   int len;               // the first new token, at most kFar
   int head, first, count;
-  int shift;             // log2 of a tile's weight: what halves the waves along the tokens
+  int shift;             // log2 of the waves along the rows (1, 2, 4)
 };
 constexpr int kFar = 1 << 29;  // past every table (2^20 pages of 128 tokens)
+
+// Units of a tile by the log2 of the waves along the rows: the time it takes.
+// 16-bit tiles come at the pace of memory until four waves share them; 4-bit
+// ones at that of the vector units nearly from the start.
+__device__ __forceinline__ int weight_of(int fmt, int shift) {
+  return fmt == DSPARK_CACHE_BF16 ? 2 + shift : (shift == 0 ? 2 : shift == 1 ? 4 : 7);
+}
+constexpr int kMinUnits = 8;  // of a work group: a tile a wave; no less than any weight
 
 __device__ __forceinline__ Block block_of(const AttnArgs& a, int entry, int rows_max) {
   const int r = entry / a.blocks, c = entry % a.blocks;
@@ -102,7 +109,7 @@ __device__ __forceinline__ Block block_of(const AttnArgs& a, int entry, int rows
     return b;
   }
   const int qt = (b.rows + kTile - 1) / kTile;
-  b.shift = max(0, (qt == 1 ? 0 : 32 - __clz(qt - 1)) - a.row_shift);
+  b.shift = qt == 1 ? 0 : 32 - __clz(qt - 1);
   const int cap = a.max_pages * a.P;
   const int end = min(b.len + (b.m0 + b.rows - 1) / a.G + 1, cap);
   const int tiles = (end + kTile - 1) / kTile;
@@ -314,8 +321,8 @@ struct Deal {
   }
 };
 
-// Whether a work group's waves share their tiles through LDS.
-constexpr bool shared_tiles(int fmt, int W) { return fmt == DSPARK_CACHE_BF16 && W == 8; }
+// Whether waves along the rows share their tiles through LDS.
+constexpr bool shared_tiles(int fmt, int D) { return fmt == DSPARK_CACHE_BF16 && D != 256; }
 
 // Moves a wave's 64 x 16 bytes from memory to LDS at byte `to`, lane by lane,
 // past the registers.  Counts as an outstanding vector load; the compiler
@@ -333,10 +340,12 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// W waves: 256 registers a wave for heads of 64 and 128 dims, so 8 waves a
-// compute unit, as one work group or two; 512 and 4 waves for 256 dims.
+// Four waves a work group.  256 registers a wave for heads of 64 and 128 dims:
+// two work groups share a compute unit, and one's startup and joining hide
+// behind the other's tiles (one of eight waves measured 3 to 15 % slower);
+// 512 registers and one work group for 256 dims.
 // TWO: pages of 16 tokens, two a tile.
-template <int FMT, int D, int W, bool TWO>
+template <int FMT, int D, bool TWO>
 __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tiles(AttnArgs a) {
   typedef PageLayout<FMT, D> L;
   constexpr int T = W * 64, NB = D / 32, KS = D / 16;
@@ -344,8 +353,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   // heads of 256 dims: the output alone takes 128 registers and a tile 128,
   // so the query rows go to LDS
   constexpr bool kQueryInLds = D == 256;
-  constexpr bool kShared = shared_tiles(FMT, W);
-  constexpr int kAlong = kShared ? 4 : W;
+  constexpr bool kShared = shared_tiles(FMT, D);
   // (the wave's own, under its output, which it writes when done with them)
   __shared__ f32x4 lds_own[W][NB * 4][64];
   __shared__ float2 lds_ml[W][64];
@@ -374,7 +382,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
       const Block b = block_of(a, e, rows_max);
-      const int64_t n = (static_cast<int64_t>(b.count) << b.shift) * a.Hkv;
+      const int64_t n = static_cast<int64_t>(b.count) * weight_of(FMT, b.shift) * a.Hkv;
       if (pass == 1 && u0 >= at + sum && u0 < at + sum + n) {
         lds_entry = e;
         lds_base = at + sum;
@@ -398,7 +406,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         N += s;
       }
       at = before + incl - sum;
-      const int64_t useful = N / a.min_units;  // a power of two
+      const int64_t useful = N / kMinUnits;
       nb = useful < 1 ? 1 : useful < gridDim.x ? static_cast<int>(useful) : static_cast<int>(gridDim.x);
       deal.share = quotient(N, nb);
       deal.rest = N - deal.share * nb;
@@ -418,7 +426,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 #pragma unroll 1
   for (int64_t u = u0; u < u1;) {
     const Block b = uniform(block_of(a, entry, rows_max));
-    const int64_t per_head = static_cast<int64_t>(b.count) << b.shift;
+    const int weight = weight_of(FMT, b.shift);
+    const int64_t per_head = static_cast<int64_t>(b.count) * weight;
     if (u >= base + per_head * a.Hkv) {
       base += per_head * a.Hkv;
       ++entry;
@@ -428,13 +437,12 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
     const int hk = uniform(static_cast<int>(quotient(u - base, per_head)));
     const int64_t seg = base + hk * per_head, seg_end = seg + per_head;
     // the tiles whose first unit is in this run
-    const int weight = 1 << b.shift;
-    const int t0 = uniform(static_cast<int>((u - seg + weight - 1) >> b.shift));
-    const int t1 = uniform(u1 < seg_end ? static_cast<int>((u1 - seg + weight - 1) >> b.shift) : b.count);
+    const int t0 = uniform(static_cast<uint32_t>(u - seg + weight - 1) / weight);
+    const int t1 = uniform(u1 < seg_end ? static_cast<uint32_t>(u1 - seg + weight - 1) / weight : b.count);
     u = seg_end;
     if (t0 >= t1) continue;
     const int qt = ceil_div(b.rows, kTile);
-    const int WT = kAlong >> b.shift;  // waves along the tokens
+    const int WT = W >> b.shift;  // waves along the tokens
     const int wt = uniform(wave / qt), wq = wave - wt * qt;
     const bool active = wt < WT;
 
@@ -590,19 +598,20 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         }
     };
 
-    if constexpr (kShared) {
-      // Rounds of WT tiles through a ring of 8 tiles in LDS.  A wave copies
-      // an eighth of every round, whole 1 KB operands in the order the lanes
+    const bool shared = kShared && b.shift > 0;
+    if constexpr (kShared) if (shared) {
+      // Rounds of WT tiles through a ring of W tiles in LDS.  A wave copies
+      // its share of every round, whole 1 KB operands in the order the lanes
       // read them, and multiplies its own tile of it.  Copies are issued
-      // 8 / WT - 1 rounds ahead, past the run's end too (its last tile
+      // W / WT - 1 rounds ahead, past the run's end too (its last tile
       // again), so that what is outstanding is known.
       constexpr int F = D / 8;  // operands of a tile: D / 16 of K, as many of V
-      static_assert(sizeof(lds_own) == 8 * F * 1024, "the ring lies under the outputs");
+      static_assert(sizeof(lds_own) == W * F * 1024, "the ring lies under the outputs");
       const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
           (__attribute__((address_space(3))) char*)(&lds_own[0][0][0])));
-      const int depth = 8 / WT, lw = __ffs(WT) - 1;
+      const int depth = W / WT, lw = __ffs(WT) - 1;
       const int rounds = (tiles + WT - 1) >> lw;
-      const int n = F * WT / 8;                   // operands a wave copies in a round
+      const int n = F * WT / W;                   // operands a wave copies in a round
       const int mine = wave * n / F, f0 = wave * n - mine * F;
       const bool keys = f0 < KS;                  // all of them K, or all V
       Ids from{-1, -1}, own{-1, -1};
@@ -636,9 +645,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 #pragma unroll 1
       for (int round = 0; round < rounds; ++round) {
         // this round's copies are there: those of the depth - 2 after it may be on their way
-        if (WT == 4) wait_and_meet<0>();
-        else if (WT == 2) wait_and_meet<2 * F / 4>();
-        else wait_and_meet<6 * F / 8>();
+        if (depth == 2) wait_and_meet<0>();
+        else wait_and_meet<2 * F / W>();
         copy(round + depth - 1);
         if ((round & 63) == 0) {
           rare();
@@ -664,7 +672,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         }
       }
       wait_and_meet<0>();
-    } else if (active && wt < tiles) {
+    }
+    if (!shared && active && wt < tiles) {
       // Every wave for itself, straight into registers, a tile ahead.
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
@@ -842,42 +851,31 @@ __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
 
 constexpr int kMaxGrid = 1024;
 
-// Waves of a work group.  A request's rows are at most this many tiles of 32;
-// a work group of 4 waves has half the startup and joining of one of 8, and
-// two of them on a compute unit overlap it; 8 waves cut the work half as
-// often and hold more rows.
-int waves_of(int gamma, int G, int D) {
-  return D == 256 || static_cast<int64_t>(gamma + 1) * G <= kTile ? 4 : 8;
-}
-
-int slot_tiles_of(int gamma, int Hq, int Hkv, int D) {
-  const int W = waves_of(gamma, Hq / Hkv, D);
+int slot_tiles_of(int gamma, int Hq, int Hkv) {
   const int64_t rows = static_cast<int64_t>(gamma + 1) * (Hq / Hkv);
   return rows >= W * kTile ? W : ceil_div(rows, kTile);
 }
 
 // Work groups: as many as the device holds at once.
-int grid_of(int gamma, int G, int D) {
-  const int per_unit = D != 256 && waves_of(gamma, G, D) == 4 ? 2 : 1;
+int grid_of(int D) {
+  const int per_unit = D == 256 ? 1 : 2;
   const int n = compute_units() * per_unit, most = kMaxGrid / 2 * per_unit;
   return n < most ? n : most;
 }
 
-template <int FMT, int D, int W, bool TWO>
+template <int FMT, int D, bool TWO>
 hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
   constexpr int NB = D / 32;
   a.page_bytes = a.Hkv * PageLayout<FMT, D>::head_bytes(a.P);
   a.blocks = ceil_div(static_cast<int64_t>(a.gamma + 1) * a.G, W * kTile);
-  a.slot_tiles = slot_tiles_of(a.gamma, a.Hq, a.Hkv, D);
-  a.min_units = W;  // no less than a tile's weight
-  a.row_shift = shared_tiles(FMT, W) ? 1 : 0;
-  const int grid = grid_of(a.gamma, a.G, D);
+  a.slot_tiles = slot_tiles_of(a.gamma, a.Hq, a.Hkv);
+  const int grid = grid_of(D);
   char* p = static_cast<char*>(ws);
   a.desc = reinterpret_cast<int32_t*>(p);
   a.ml = reinterpret_cast<float2*>(p + kMaxGrid * sizeof(Desc));
   a.part = reinterpret_cast<float*>(p + kMaxGrid * sizeof(Desc) +
                                     static_cast<size_t>(grid) * 2 * a.slot_tiles * kTile * sizeof(float2));
-  cache_attention_tiles<FMT, D, W, TWO><<<grid, W * 64, 0, s>>>(a);
+  cache_attention_tiles<FMT, D, TWO><<<grid, W * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // few heads and requests: many parts each
@@ -888,17 +886,13 @@ hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
 }
 
 template <int FMT, int D>
-hipError_t run_w(AttnArgs& a, void* ws, hipStream_t s) {
-  if constexpr (D != 256) {
-    if (waves_of(a.gamma, a.G, D) == 8)
-      return a.P == 16 ? run<FMT, D, 8, true>(a, ws, s) : run<FMT, D, 8, false>(a, ws, s);
-  }
-  return a.P == 16 ? run<FMT, D, 4, true>(a, ws, s) : run<FMT, D, 4, false>(a, ws, s);
+hipError_t run_p(AttnArgs& a, void* ws, hipStream_t s) {
+  return a.P == 16 ? run<FMT, D, true>(a, ws, s) : run<FMT, D, false>(a, ws, s);
 }
 
 template <int FMT>
 hipError_t run_d(int D, AttnArgs& a, void* ws, hipStream_t s) {
-  return D == 64 ? run_w<FMT, 64>(a, ws, s) : D == 128 ? run_w<FMT, 128>(a, ws, s) : run_w<FMT, 256>(a, ws, s);
+  return D == 64 ? run_p<FMT, 64>(a, ws, s) : D == 128 ? run_p<FMT, 128>(a, ws, s) : run_p<FMT, 256>(a, ws, s);
 }
 
 }  // namespace
@@ -906,9 +900,8 @@ hipError_t run_d(int D, AttnArgs& a, void* ws, hipStream_t s) {
 size_t cache_attention_workspace_bytes(int R, int gamma, int Hq, int Hkv, int D) {
   (void)R;
   // sized for the largest grid: the size does not depend on the device
-  const int W = waves_of(gamma, Hq / Hkv, D);
-  const size_t grid = D != 256 && W == 4 ? kMaxGrid : kMaxGrid / 2;
-  const size_t rows = grid * 2 * slot_tiles_of(gamma, Hq, Hkv, D) * kTile;
+  const size_t grid = D == 256 ? kMaxGrid / 2 : kMaxGrid;
+  const size_t rows = grid * 2 * slot_tiles_of(gamma, Hq, Hkv) * kTile;
   return kMaxGrid * sizeof(Desc) + rows * (sizeof(float2) + static_cast<size_t>(D) * sizeof(float));
 }
 
