@@ -36,6 +36,7 @@ struct AttnArgs {
   int R, gamma, Hq, Hkv, G, P, n_pages, max_pages;
   int blocks;              // row blocks a request can have
   int slot_tiles;          // row tiles of a workspace slot
+  int by_head;             // descriptors per (request, row block, head), not per work group
   const uint16_t* q;
   float scale_log2;        // |scale| log2(e) (1 for a zero scale, with q masked to zero)
   uint32_t q_keep, q_flip; // q & keep ^ flip: the scale's sign, or zero
@@ -51,13 +52,15 @@ struct AttnArgs {
   float* part;
 };
 
-// What a work group leaves for the join: the part it opened but did not close.
+// What is left for the join: a (row block, head) that work group `wg` opened
+// and did not close, in `parts` parts of as many work groups.
 struct Desc {
   int parts;     // 0: nothing
   int rows, m0;  // the row block
   int head;
   int64_t first_row;  // the request's row 0 in q and out
-  int64_t pad;
+  int wg;
+  int pad;
 };
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 x) {
@@ -311,6 +314,14 @@ __device__ __forceinline__ void add_non_finite(f32x16 (&o)[D / 32], const float 
   }
 }
 
+// What starting another head costs a work group, in units (5 us of them).
+constexpr int kRestart = 16;
+
+// Tiles of a part of a head in `parts` parts, the last ones perhaps empty.
+__device__ __forceinline__ int part_tiles(int count, int weight, int parts) {
+  return max((count + parts - 1) / parts, (kMinUnits + weight - 1) / weight);
+}
+
 // The range of units of work group wg: `share` each, the first `rest` one more.
 struct Deal {
   int64_t share, rest;
@@ -359,7 +370,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   __shared__ float2 lds_ml[W][64];
   static_assert(NB * 4 >= KS && (NB * 4) % W == 0, "the queries fit under the output; waves share its pieces");
   __shared__ int64_t lds_scan[W];
-  __shared__ int64_t lds_base;
+  __shared__ int64_t lds_base, lds_run[2];
+  __shared__ int2 lds_heads[W];
   __shared__ int lds_entry;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, col = lane & 31;
@@ -367,59 +379,103 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   const int wg = blockIdx.x;
 
   // Units before every entry (request, row block): runs of entries per
-  // thread and a scan.  A tile counts once per wave along the rows, the time
-  // it takes.  The second pass looks up where this work group's run begins.
+  // thread and a scan, with the heads (an entry has a.Hkv) and the longest
+  // head beside it.  Then the deal: equal runs of units whatever their
+  // owners, or, if the heads are few and of one length, whole parts of heads,
+  // which a work group starts and ends once.  A further pass looks up where
+  // this work group's run begins.
   const int entries = a.R * a.blocks;
   const int per = ceil_div(entries, T);
   const int e0 = min(entries, static_cast<int>(threadIdx.x) * per), e1 = min(entries, e0 + per);
+  if (threadIdx.x == 0) lds_run[0] = lds_run[1] = 0;
   Deal deal{0, 0};
-  int64_t at = 0, u0 = 0, u1 = 0;
-  int nb = 0;
+  int64_t at = 0, u0 = 0;
+  int nb = 0, parts = 0;  // parts of a head; 0: equal runs
+  int heads_at = 0, my_head = 0, my_part = 0;
+  auto place = [&](int e, int64_t units_at, int first_head, int count, int weight) {
+    const int64_t per_head = static_cast<int64_t>(count) * weight;
+    if (parts > 0) {
+      const int x = my_head - first_head;
+      if (count == 0 || x < 0 || x >= a.Hkv) return;
+      const int c = part_tiles(count, weight, parts);
+      lds_entry = e;
+      lds_base = units_at;
+      lds_run[0] = units_at + x * per_head + min(static_cast<int64_t>(my_part) * c, static_cast<int64_t>(count)) * weight;
+      lds_run[1] =
+          units_at + x * per_head + min((my_part + 1) * static_cast<int64_t>(c), static_cast<int64_t>(count)) * weight;
+    } else if (u0 >= units_at && u0 < units_at + per_head * a.Hkv) {
+      lds_entry = e;
+      lds_base = units_at;
+      lds_run[0] = u0;
+      lds_run[1] = wg < nb ? deal.begin(wg + 1) : u0;
+    }
+  };
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1 && per == 1) break;
     int64_t sum = 0;
+    int heads = 0, longest = 0, count = 0, weight = 1;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
       const Block b = block_of(a, e, rows_max);
-      const int64_t n = static_cast<int64_t>(b.count) * weight_of(FMT, b.shift) * a.Hkv;
-      if (pass == 1 && u0 >= at + sum && u0 < at + sum + n) {
-        lds_entry = e;
-        lds_base = at + sum;
-      }
-      sum += n;
+      count = b.count;
+      weight = weight_of(FMT, b.shift);
+      if (pass == 1) place(e, at + sum, heads_at + heads, count, weight);
+      else if (count == 0 && a.by_head && wg == 0)  // nobody opens these
+        for (int x = 0; x < a.Hkv; ++x) reinterpret_cast<Desc*>(a.desc)[e * a.Hkv + x].parts = 0;
+      sum += static_cast<int64_t>(count) * weight * a.Hkv;
+      heads += count > 0 ? a.Hkv : 0;
+      longest = max(longest, count * weight);
     }
     if (pass == 0) {
       int64_t incl = sum;
+      int heads_incl = heads;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int64_t t = __shfl_up(incl, o);
-        if (lane >= o) incl += t;
+        const int n = __shfl_up(heads_incl, o);
+        if (lane >= o) incl += t, heads_incl += n;
+        longest = max(longest, __shfl_xor(longest, o));
       }
-      if (lane == 63) lds_scan[wave] = incl;
+      if (lane == 63) {
+        lds_scan[wave] = incl;
+        lds_heads[wave] = make_int2(heads_incl, longest);
+      }
       __syncthreads();
       int64_t before = 0, N = 0;
+      int heads_before = 0, H = 0;
+      longest = 0;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const int64_t s = lds_scan[w];
-        if (w < wave) before += s;
+        const int2 n = lds_heads[w];
+        if (w < wave) before += s, heads_before += n.x;
         N += s;
+        H += n.x;
+        longest = max(longest, n.y);
       }
       at = before + incl - sum;
+      heads_at = heads_before + heads_incl - heads;
       const int64_t useful = N / kMinUnits;
       nb = useful < 1 ? 1 : useful < gridDim.x ? static_cast<int>(useful) : static_cast<int>(gridDim.x);
       deal.share = quotient(N, nb);
       deal.rest = N - deal.share * nb;
       u0 = deal.begin(wg);
-      u1 = wg < nb ? deal.begin(wg + 1) : u0;
-      if (per == 1 && u0 >= at && u0 < at + sum) {
-        lds_entry = e0;
-        lds_base = at;
+      if (H > 0 && H <= static_cast<int>(gridDim.x)) {
+        const int p = min(static_cast<int>(gridDim.x / H), ceil_div(longest, kMinUnits));
+        if (longest / p <= deal.share + kRestart) {
+          parts = p;
+          my_head = wg / p;
+          my_part = wg - my_head * p;
+        }
       }
+      if (per == 1 && e0 < e1) place(e0, at, heads_at, count, weight);
     }
   }
   __syncthreads();
   Desc left{};
+  u0 = lds_run[0];
+  const int64_t u1 = lds_run[1];
   int entry = u0 < u1 ? __builtin_amdgcn_readfirstlane(lds_entry) : 0;
   int64_t base = u0 < u1 ? lds_base : 0;
 
@@ -774,59 +830,70 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       }
     }
     __syncthreads();  // before the next segment's waves write there
-    if (opens && !closes)  // the work group that holds the last tile's first unit has the last part
-      left = Desc{deal.owner(seg_end - weight) - wg + 1, b.rows, b.m0, hk, first_row, 0};
+    if (opens) {  // the work group that holds the last tile's first unit has the last part
+      const int n = closes ? 0
+                    : parts > 0 ? ceil_div(b.count, part_tiles(b.count, weight, parts))
+                                : deal.owner(seg_end - weight) - wg + 1;
+      left = Desc{n, b.rows, b.m0, hk, first_row, wg, 0};
+      if (a.by_head && threadIdx.x == 0) reinterpret_cast<Desc*>(a.desc)[entry * a.Hkv + hk] = left;
+    }
   }
-  if (threadIdx.x == 0) reinterpret_cast<Desc*>(a.desc)[wg] = left;
+  if (!a.by_head && threadIdx.x == 0) reinterpret_cast<Desc*>(a.desc)[wg] = left;
 }
 
-// Joins the parts of what a work group opened and did not close, in the order
-// of the tokens.  A wave takes 4 output dims of 32 rows per half (a piece, as
-// the parts were stored); with many parts (SPLIT 4) the four waves of a block
-// take a quarter of one piece's parts each.  The pieces of one work group are
-// consecutive blocks, so that they spread over the dies: what is left open is
-// often a few work groups whose indices are multiples of 8.
+// Joins the parts of a descriptor in the order of the tokens.  A piece is 4
+// output dims of 32 rows per half of a wave, as the parts were stored.
+// Few parts (SPLIT 1): a block per row tile, NB pieces a wave, their loads
+// together.  Many (SPLIT 4): a block per piece, each wave a quarter of the
+// parts, joined in LDS.
 template <int D, int SPLIT>
 __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
-  constexpr int NB = D / 32;
+  constexpr int NB = D / 32, PIECES = SPLIT == 1 ? NB : 1;
   __shared__ f32x4 lds_o[SPLIT == 1 ? 1 : 4][64];
   __shared__ float2 lds_ml[SPLIT == 1 ? 1 : 4][64];
-  const int per_wg = a.slot_tiles * NB * SPLIT;
-  const int wg = blockIdx.x / per_wg;
-  const Desc d = reinterpret_cast<const Desc*>(a.desc)[wg];
+  const int per_desc = a.slot_tiles * (SPLIT == 1 ? 1 : NB * 4);
+  const Desc d = reinterpret_cast<const Desc*>(a.desc)[blockIdx.x / per_desc];
   if (d.parts == 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int piece = SPLIT == 1 ? (blockIdx.x % per_wg) * 4 + wave : blockIdx.x % per_wg;
-  const int wq = piece / (NB * 4), x = piece % (NB * 4);
+  const int at = blockIdx.x % per_desc;
+  const int wq = SPLIT == 1 ? at : at / (NB * 4);
+  const int x0 = SPLIT == 1 ? wave * NB : at % (NB * 4);
   const int row = wq * kTile + (lane & 31);
   if (wq * kTile >= d.rows) return;
   const int each = SPLIT == 1 ? d.parts : ceil_div(d.parts, SPLIT);
   const int k_first = SPLIT == 1 ? 0 : wave * each, k_end = min(d.parts, k_first + each);
   float m = neg_inf(), l = 0.f;
-  f32x4 o{0.f, 0.f, 0.f, 0.f};
-  auto add = [&](float2 ml, f32x4 y) {
+  f32x4 o[PIECES];
+#pragma unroll
+  for (int x = 0; x < PIECES; ++x) o[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto add = [&](float2 ml, const f32x4* y) {
     const float top = fmaxf(m, ml.x), ref = top == neg_inf() ? 0.f : top;
     const float sa = __builtin_amdgcn_exp2f(m - ref), sb = __builtin_amdgcn_exp2f(ml.x - ref);
     m = top;
     l = l * sa + ml.y * sb;
 #pragma unroll
-    for (int z = 0; z < 4; ++z) o[z] = o[z] * sa + y[z] * sb;
+    for (int x = 0; x < PIECES; ++x)
+#pragma unroll
+      for (int z = 0; z < 4; ++z) o[x][z] = o[x][z] * sa + y[x][z] * sb;
   };
-  // four parts' loads at a time: the loop is a chain of latencies otherwise
-  constexpr int kBatch = 4;
+  // several parts' loads at a time: the loop is a chain of latencies otherwise
+  constexpr int kBatch = SPLIT == 1 ? 2 : 4;
 #pragma unroll 1
   for (int k0 = k_first; k0 < k_end; k0 += kBatch) {
     float2 ml[kBatch];
-    f32x4 y[kBatch];
+    f32x4 y[kBatch][PIECES];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int k = k0 + j;
       ml[j] = make_float2(neg_inf(), 0.f);
-      y[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < PIECES; ++x) y[j][x] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (k < k_end && row < d.rows) {
-        const int64_t slot = (static_cast<int64_t>(wg + k) * 2 + (k == 0 ? 1 : 0)) * a.slot_tiles + wq;
+        const int64_t slot = (static_cast<int64_t>(d.wg + k) * 2 + (k == 0 ? 1 : 0)) * a.slot_tiles + wq;
         ml[j] = a.ml[slot * kTile + (lane & 31)];
-        y[j] = reinterpret_cast<const f32x4*>(a.part)[slot * (NB * 4 * 64) + x * 64 + lane];
+#pragma unroll
+        for (int x = 0; x < PIECES; ++x)
+          y[j][x] = reinterpret_cast<const f32x4*>(a.part)[slot * (NB * 4 * 64) + (x0 + x) * 64 + lane];
       }
     }
 #pragma unroll
@@ -834,19 +901,23 @@ __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
   }
   if constexpr (SPLIT > 1) {
     lds_ml[wave][lane] = make_float2(m, l);
-    lds_o[wave][lane] = o;
+    lds_o[wave][lane] = o[0];
     __syncthreads();
     if (wave != 0) return;
 #pragma unroll
-    for (int k = 1; k < SPLIT; ++k) add(lds_ml[k][lane], lds_o[k][lane]);
+    for (int k = 1; k < SPLIT; ++k) add(lds_ml[k][lane], &lds_o[k][lane]);
   }
   if (row >= d.rows) return;
   const int i = (d.m0 + row) / a.G, g = (d.m0 + row) - i * a.G;
   const int64_t out_at = (d.first_row + i) * a.Hq + d.head * a.G + g;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  const u32x2 w{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
-  *reinterpret_cast<u32x2*>(a.out + out_at * D + (x / 4) * 32 + 8 * (x % 4) + 4 * (lane >> 5)) = w;
-  if (a.lse && x == 0 && lane < 32) a.lse[out_at] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) {
+    const int x = x0 + j;
+    const u32x2 w{bf16_pair(o[j][0] * inv, o[j][1] * inv), bf16_pair(o[j][2] * inv, o[j][3] * inv)};
+    *reinterpret_cast<u32x2*>(a.out + out_at * D + (x / 4) * 32 + 8 * (x % 4) + 4 * (lane >> 5)) = w;
+  }
+  if (a.lse && x0 == 0 && lane < 32) a.lse[out_at] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
 }
 
 constexpr int kMaxGrid = 1024;
@@ -870,6 +941,9 @@ hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
   a.blocks = ceil_div(static_cast<int64_t>(a.gamma + 1) * a.G, W * kTile);
   a.slot_tiles = slot_tiles_of(a.gamma, a.Hq, a.Hkv);
   const int grid = grid_of(D);
+  // few heads and requests: many parts each
+  const int64_t heads = static_cast<int64_t>(a.R) * a.blocks * a.Hkv;
+  a.by_head = heads * 4 <= grid;
   char* p = static_cast<char*>(ws);
   a.desc = reinterpret_cast<int32_t*>(p);
   a.ml = reinterpret_cast<float2*>(p + kMaxGrid * sizeof(Desc));
@@ -878,10 +952,8 @@ hipError_t run(AttnArgs& a, void* ws, hipStream_t s) {
   cache_attention_tiles<FMT, D, TWO><<<grid, W * 64, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // few heads and requests: many parts each
-  const bool many = static_cast<int64_t>(a.R) * a.blocks * a.Hkv * 4 <= grid;
-  if (many) cache_attention_join<D, 4><<<grid * a.slot_tiles * NB * 4, 256, 0, s>>>(a);
-  else cache_attention_join<D, 1><<<grid * a.slot_tiles * NB, 256, 0, s>>>(a);
+  if (a.by_head) cache_attention_join<D, 4><<<heads * a.slot_tiles * NB * 4, 256, 0, s>>>(a);
+  else cache_attention_join<D, 1><<<grid * a.slot_tiles, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
