@@ -332,8 +332,12 @@ struct Deal {
   }
 };
 
-// Whether waves along the rows share their tiles through LDS.
-constexpr bool shared_tiles(int fmt, int D) { return fmt == DSPARK_CACHE_BF16 && D != 256; }
+// Waves along the tokens by the log2 of those along the rows.  Of 16-bit
+// heads of 256 dims no tile fits the registers beside the output, so theirs
+// all come through LDS, and the ring there holds two rounds of two.
+__device__ __forceinline__ int waves_along(int fmt, int D, int shift) {
+  return fmt == DSPARK_CACHE_BF16 && D == 256 ? min(2, W >> shift) : W >> shift;
+}
 
 // Moves a wave's 64 x 16 bytes from memory to LDS at byte `to`, lane by lane,
 // past the registers.  Counts as an outstanding vector load; the compiler
@@ -361,10 +365,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   typedef PageLayout<FMT, D> L;
   constexpr int T = W * 64, NB = D / 32, KS = D / 16;
   constexpr float kSlack = 8.f;  // a weight may reach 2^8 before the sums are rescaled
-  // heads of 256 dims: the output alone takes 128 registers and a tile 128,
-  // so the query rows go to LDS
-  constexpr bool kQueryInLds = D == 256;
-  constexpr bool kShared = shared_tiles(FMT, D);
+  // 4-bit heads of 256 dims: output and tiles leave no registers for the query rows
+  constexpr bool kQueryInLds = D == 256 && FMT == DSPARK_CACHE_FP4;
+  constexpr bool kShared = FMT == DSPARK_CACHE_BF16;
   // (the wave's own, under its output, which it writes when done with them)
   __shared__ f32x4 lds_own[W][NB * 4][64];
   __shared__ float2 lds_ml[W][64];
@@ -498,7 +501,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
     u = seg_end;
     if (t0 >= t1) continue;
     const int qt = ceil_div(b.rows, kTile);
-    const int WT = W >> b.shift;  // waves along the tokens
+    const int WT = waves_along(FMT, D, b.shift);
     const int wt = uniform(wave / qt), wq = wave - wt * qt;
     const bool active = wt < WT;
 
@@ -654,7 +657,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         }
     };
 
-    const bool shared = kShared && b.shift > 0;
+    const bool shared = kShared && (D == 256 || b.shift > 0);
     if constexpr (kShared) if (shared) {
       // Rounds of WT tiles through a ring of W tiles in LDS.  A wave copies
       // its share of every round, whole 1 KB operands in the order the lanes
@@ -729,7 +732,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       }
       wait_and_meet<0>();
     }
-    if (!shared && active && wt < tiles) {
+    if constexpr (D != 256 || !kShared) if (!shared && active && wt < tiles) {
       // Every wave for itself, straight into registers, a tile ahead.
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
