@@ -2,13 +2,21 @@
 // and the new tokens' K and V into the cache's pages; cached tokens back out
 // as dense rows (include/dspark_cache.h).
 //
-// A work group takes the (at most 8) new tokens of one request that share an
-// aligned group of 8 tokens: V is stored with a dim's 8 tokens together, so
-// the group owns the 16-byte (4-bit: 4-byte) words it writes.  D / 8 lanes
-// hold a head, 8 dims each: 16-byte loads, the sum of squares over those
+// A group is the (at most 8) new tokens of one request that share an aligned
+// group of 8 tokens: V is stored with a dim's 8 tokens together, so whoever
+// works on the group owns the 16-byte (4-bit: 4-byte) words it writes.  D / 8
+// lanes hold a head, 8 dims each: 16-byte loads, the sum of squares over those
 // lanes, the rotation's partner a shuffle away (or in the same lane for
-// adjacent pairs).  Sines and cosines of the group's positions are made once
-// per work group in LDS and serve all heads.
+// adjacent pairs).  Several work groups share a group's heads, each a
+// contiguous run of them, so that each makes the sines and cosines of the few
+// rows it works on, in LDS, for all its heads.
+//
+// Latency bounds it: a chain of loads (the length, the page's id, the row),
+// the sines, one pass over the rows.  GPU time with heads of 128 dims and 8
+// heads of keys: one token, 32 query heads, 3.9 us (the sines and what comes
+// before them 2.9); 128 requests of up to 17 packed rows, 56 query heads,
+// 15.6 us, of which V of groups that are not whole, in 2-byte stores, is 1.8;
+// 32 requests x 17 rows into 4-bit pages 12.6 us; 4 x 512 rows 15.6 us.
 #include "cache.hpp"
 
 namespace dspark {
@@ -30,31 +38,39 @@ struct AppendArgs {
   uint16_t* q_out;
   char* pool;
   int64_t page_bytes;
+  int page_shift;
+  float per_q, per_k, per_half;  // 1 / Hq, 1 / Hkv, 1 / (rot / 2)
 };
+
+// x / y for 0 <= x < 2^14, 1 <= y <= 2^10 and inv = 1 / y in fp32: x + 1/2 is
+// at least 1 / (2 y) from a multiple of y, far more than the product's error.
+__device__ __forceinline__ int small_quotient(int x, float inv) {
+  return static_cast<int>((static_cast<float>(x) + 0.5f) * inv);
+}
 
 __device__ __forceinline__ double shfl_xor_t(double x, int o) { return __shfl_xor(x, o); }
 __device__ __forceinline__ float shfl_xor_t(float x, int o) { return __shfl_xor(x, o); }
 
-__device__ __forceinline__ float inv_sqrt(float x) { return 1.f / sqrtf(x); }
+__device__ __forceinline__ float inv_sqrt(float x) { return rsqrtf(x); }
 __device__ __forceinline__ double inv_sqrt(double x) { return 1.0 / sqrt(x); }
 
 // The norm and the rotation of one head, 8 dims per lane, in the type T.
-// li: the lane's place in the head; cs: cosine and sine of pair i at 2 i.
+// li: the lane's place in the head; w: the norm's weights of its dims; cs:
+// cosine and sine of pair i at 2 i.
 template <typename T, int D>
-__device__ __forceinline__ void norm_rotate(T (&x)[8], int li, const uint16_t* w, float eps, int rot, bool adjacent,
-                                            const T* cs) {
+__device__ __forceinline__ void norm_rotate(T (&x)[8], int li, bool norm, const u32x4& w, float eps, int rot,
+                                            bool adjacent, const T* cs) {
   constexpr int L = D / 8;
-  if (w) {
+  if (norm) {
     T ss = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) ss += shfl_xor_t(ss, o);
     const T s = inv_sqrt(ss * static_cast<T>(1.0 / D) + static_cast<T>(eps));
-    const u32x4 wv = *reinterpret_cast<const u32x4*>(w + li * 8);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      x[e] = x[e] * s * static_cast<T>(bf16_to_f32(static_cast<uint16_t>(wv[e / 2] >> (16 * (e & 1)))));
+      x[e] = x[e] * s * static_cast<T>(bf16_to_f32(static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)))));
   }
   if (rot == 0) return;
   if (adjacent) {
@@ -156,71 +172,103 @@ __device__ __forceinline__ void store_v8_bf16(const uint16_t* src, int64_t ldv, 
   }
 }
 
-// .. or one token, whose neighbours in those 16 bytes stay as they are.
-__device__ __forceinline__ void store_v1_bf16(const uint16_t* src, char* dst) {
-  const u32x4 x = *reinterpret_cast<const u32x4*>(src);
+// .. or one token, whose neighbours in those 16 bytes stay as they are: a
+// lane takes dims li, li + L, .., so that a store's lanes lie side by side
+// (eight dims a line) and not a line apart.
+template <int D>
+__device__ __forceinline__ void store_v1_bf16(const uint16_t* src, int li, char* dst) {
+  constexpr int L = D / 8;
+  uint16_t x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    *reinterpret_cast<uint16_t*>(dst + 16 * e) = static_cast<uint16_t>(x[e / 2] >> (16 * (e & 1)));
+  for (int e = 0; e < 8; ++e) x[e] = src[e * L + li];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) *reinterpret_cast<uint16_t*>(dst + 16 * (e * L + li)) = x[e];
 }
 
-// V of one head of a 4-bit page: tokens first .. first + n - 1 of the group
-// of 8 at src, a dim's 8 codes in one word; words with other tokens in them
-// are read and merged.
+// V of one head of a 4-bit page, a token a head slot: the slots of a wave
+// hold 64 / (D / 8) tokens of the group in turn, make their codes, and put
+// them together into the part of a dim's word that these tokens fill: 4, 2 or
+// 1 bytes for heads of 64, 128 and 256 dims.  src: the lane's 8 dims of token
+// j if that is new (j in first .. first + n - 1), else unused.
 template <int D>
-__device__ __forceinline__ void store_v_fp4(const uint16_t* src, int64_t ldv, int li, int first, int n, char* head,
-                                            int P, int t8) {
+__device__ __forceinline__ void store_v_fp4(const uint16_t* src, int li, int j, int first, int n, char* head, int P,
+                                            int t8) {
   typedef PageLayout<DSPARK_CACHE_FP4, D> L;
-  u32x4 x[kGroup];
+  constexpr int kLanes = D / 8, kTokens = 64 / kLanes;
+  const bool mine = j >= first && j < first + n;
+  u32x4 x{0u, 0u, 0u, 0u};
+  if (mine) x = *reinterpret_cast<const u32x4*>(src);
+  float f[8], top = 0.f;
+  bool bad = false;
+  unpack(x, f);
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) {
-    x[j] = u32x4{0u, 0u, 0u, 0u};
-    if (j >= first && j < first + n) x[j] = *reinterpret_cast<const u32x4*>(src + (j - first) * ldv);
+  for (int e = 0; e < 8; ++e) {
+    top = fmaxf(top, fabsf(f[e]));
+    bad |= !(fabsf(f[e]) <= 3.4028234e38f);
   }
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) {
+    top = fmaxf(top, __shfl_xor(top, o));
+    bad |= __shfl_xor(static_cast<int>(bad), o) != 0;
+  }
+  // 6 |v| against the borders times max |v|: products of 16-bit values with
+  // numbers of at most 3 bits, exact in fp32; above 2^100 both sides are
+  // scaled down first so that they stay finite
+  const float sc = top > 1.2676506e30f ? 7.8886091e-31f : 1.f;
+  const int j0 = j & ~(kTokens - 1), at = 4 * (j - j0);
   uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = 0;
+  for (int e = 0; e < 8; ++e) w[e] = (bad || top == 0.f ? 0u : code_of(6.f * (f[e] * sc), top * sc)) << at;
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) {
-    if (j < first || j >= first + n) continue;  // the same for all lanes of the head
-    float f[8], top = 0.f;
-    bool bad = false;
-    unpack(x[j], f);
+  for (int o = kLanes; o < 64; o <<= 1)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      top = fmaxf(top, fabsf(f[e]));
-      bad |= !(fabsf(f[e]) <= 3.4028234e38f);
+    for (int e = 0; e < 8; ++e) w[e] |= static_cast<uint32_t>(__shfl_xor(static_cast<int>(w[e]), o));
+  if (mine && li == 0) *reinterpret_cast<float*>(head + L::v_scale(P, t8 + j)) = bad ? __builtin_nanf("") : top / 6.f;
+  // bits of the new tokens among these; each slot stores its share of the 8 dims
+  const int lo = max(first, j0) - j0, hi = min(first + n, j0 + kTokens) - j0;
+  if (lo >= hi) return;
+  const uint32_t bits = static_cast<uint32_t>(((1ull << (4 * (hi - lo))) - 1ull) << (4 * lo));
+  const int part = j - j0;
+  char* p = head + L::v(P, t8, li * 8) + j0 / 2;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e % kTokens == part) {
+      // dims 8 li .. of a group of 32 are consecutive in the first of the two dim axes
+      char* q = p + e * (4 * L::E);
+      if constexpr (kTokens == 8) {
+        uint32_t* z = reinterpret_cast<uint32_t*>(q);
+        *z = hi - lo == 8 ? w[e] : (*z & ~bits) | w[e];
+      } else if constexpr (kTokens == 4) {
+        uint16_t* z = reinterpret_cast<uint16_t*>(q);
+        *z = static_cast<uint16_t>(hi - lo == 4 ? w[e] : (*z & ~bits) | w[e]);
+      } else {
+        uint8_t* z = reinterpret_cast<uint8_t*>(q);
+        *z = static_cast<uint8_t>(hi - lo == 2 ? w[e] : (*z & ~bits) | w[e]);
+      }
     }
-#pragma unroll
-    for (int o = 1; o < D / 8; o <<= 1) {
-      top = fmaxf(top, __shfl_xor(top, o));
-      bad |= __shfl_xor(static_cast<int>(bad), o) != 0;
-    }
-    // 6 |v| against the borders times max |v|: products of 16-bit values with
-    // numbers of at most 3 bits, exact in fp32; above 2^100 both sides are
-    // scaled down first so that they stay finite
-    const float sc = top > 1.2676506e30f ? 7.8886091e-31f : 1.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w[e] |= (bad || top == 0.f ? 0u : code_of(6.f * (f[e] * sc), top * sc)) << (4 * j);
-    if (li == 0) *reinterpret_cast<float*>(head + L::v_scale(P, t8 + j)) = bad ? __builtin_nanf("") : top / 6.f;
-  }
-  const uint32_t mine = static_cast<uint32_t>(((1ull << (4 * n)) - 1ull) << (4 * first));
-  // dims 8 li .. of a group of 32: consecutive in the first of the two dim axes
-  uint32_t* p = reinterpret_cast<uint32_t*>(head + L::v(P, t8, li * 8));
-#pragma unroll
-  for (int e = 0; e < 8; ++e) p[e * L::E] = n == kGroup ? w[e] : (p[e * L::E] & ~mine) | w[e];
 }
 
+// A unit is a head slot's work: one head of one row for q and k; V of a 16-bit
+// page by head (whole groups) or head and row, of a 4-bit page by head and
+// token of the group.  In that order, so that the fp64 angles of 4-bit keys
+// are made by the few work groups that hold such units.
 template <int FMT, int D>
 __global__ __launch_bounds__(kThreads, 4) void cache_append_kernel(AppendArgs a) {
   constexpr int L = D / 8, kHeads = kThreads / L;  // head slots of the work group
-  // keys of 4-bit pages need fp64 sines as well
   __shared__ float cs[kGroup * D];
   __shared__ double cs64[FMT == DSPARK_CACHE_FP4 ? kGroup * D : 1];
-  const int r = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
+  const int r = blockIdx.z, g = blockIdx.x;
+  const int half = a.rot / 2;
+  // what does not depend on anything, at once
   const int n_rows = rows_of(a.ell[r], a.gamma);
   const int64_t len = a.len[r];
+  const int64_t row0 = a.row0 ? static_cast<int64_t>(a.row0[r]) : static_cast<int64_t>(r) * (a.gamma + 1);
+  const int pair0 = threadIdx.x - small_quotient(threadIdx.x, a.per_half) * half;
+  const double freq0 = half ? a.freq[pair0] : 0.0;
+  const int li = threadIdx.x % L;
+  u32x4 w_q{0u, 0u, 0u, 0u}, w_k{0u, 0u, 0u, 0u};
+  if (a.wq) w_q = *reinterpret_cast<const u32x4*>(a.wq + li * 8);
+  if (a.wk) w_k = *reinterpret_cast<const u32x4*>(a.wk + li * 8);
   if (len < 0) return;
   // tokens [t0, t1) of this group
   const int64_t base = (len / kGroup + g) * kGroup;
@@ -228,82 +276,81 @@ __global__ __launch_bounds__(kThreads, 4) void cache_append_kernel(AppendArgs a)
   const int64_t t1 = base + kGroup < len + n_rows ? base + kGroup : len + n_rows;
   if (t0 >= t1) return;
   const int n = static_cast<int>(t1 - t0), first = static_cast<int>(t0 - base);
-  const int64_t row_first =
-      (a.row0 ? static_cast<int64_t>(a.row0[r]) : static_cast<int64_t>(r) * (a.gamma + 1)) + (t0 - len);
-  const int64_t slot = base / a.P;
+  const int nq = n * a.Hq, nqk = nq + n * a.Hkv;
+  const bool whole = n == kGroup;
+  const int v0 = FMT == DSPARK_CACHE_FP4 ? (nqk + kGroup - 1) / kGroup * kGroup : nqk;
+  const int units = v0 + (FMT == DSPARK_CACHE_FP4 ? a.Hkv * kGroup : whole ? a.Hkv : n * a.Hkv);
+  // this work group's run of them, whole rounds of kHeads
+  const int rounds = ceil_div(units, kHeads * static_cast<int>(gridDim.y));
+  const int u_lo = blockIdx.y * rounds * kHeads, u_hi = min(units, u_lo + rounds * kHeads);
+  if (u_lo >= u_hi) return;
+  const int64_t row_first = row0 + (t0 - len);
+  const int64_t slot = base >> a.page_shift;
   const int id = slot < a.max_pages ? page_or_none(a.table[static_cast<int64_t>(r) * a.max_pages + slot], a.n_pages)
                                     : -1;
-  const int t8 = static_cast<int>(base % a.P);
+  const int t8 = static_cast<int>(base & (a.P - 1));
   char* page = id >= 0 ? a.pool + id * a.page_bytes : nullptr;
 
-  // a unit is one head of one row (q, k, and V one row at a time), or V of a
-  // head for a whole group; every lane of a head slot takes the same unit, so
-  // the shuffles inside a head are whole
-  const int li = threadIdx.x % L;
-  const int per_row = a.Hq + a.Hkv;
-  const bool whole = FMT == DSPARK_CACHE_FP4 || n == kGroup;
-  const int units = n * per_row + (whole ? a.Hkv : n * a.Hkv);
-  int u = blockIdx.y * kHeads + threadIdx.x / L;
-  // V and the first row need no angles: they are on their way while those are made
-  auto row_of = [&](int unit, const uint16_t** src) {
-    const int j = unit / per_row, head = unit - j * per_row;
-    *src = head < a.Hq ? a.q + (row_first + j) * a.ldq + head * D
-                       : a.k + (row_first + j) * a.ldk + (head - a.Hq) * D;
-    return j;
+  // row and source of a q or k unit
+  auto row_of = [&](int u) { return u < nq ? small_quotient(u, a.per_q) : small_quotient(u - nq, a.per_k); };
+  auto source = [&](int u, int j) {
+    return u < nq ? a.q + (row_first + j) * a.ldq + (u - j * a.Hq) * D
+                  : a.k + (row_first + j) * a.ldk + (u - nq - j * a.Hkv) * D;
   };
-  u32x4 raw{0u, 0u, 0u, 0u};
-  if (u < n * per_row) {
-    const uint16_t* src;
-    row_of(u, &src);
-    raw = *reinterpret_cast<const u32x4*>(src + li * 8);
-  }
-  const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int row = i / half, p = i - row * half;
-    const double turns = static_cast<double>(t0 + row) * a.freq[p] * 0.15915494309189535;
+  int u = u_lo + threadIdx.x / L;
+  u32x4 raw{0u, 0u, 0u, 0u};  // the next q or k unit's values, loaded a round ahead
+  if (u < min(u_hi, nqk)) raw = *reinterpret_cast<const u32x4*>(source(u, row_of(u)) + li * 8);
+
+  // sines and cosines of the rows of this run's q and k units
+  const bool has_q = u_lo < nq, has_k = u_hi > nq && u_lo < nqk;
+  const int k_a = has_k ? row_of(max(u_lo, nq)) : 0, k_b = has_k ? row_of(min(u_hi, nqk) - 1) : -1;
+  const int q_a = has_q ? row_of(u_lo) : k_a, q_b = has_q ? row_of(min(u_hi, nq) - 1) : k_b;
+  const int j_a = has_k ? min(q_a, k_a) : q_a, j_b = max(q_b, k_b);
+  for (int i = threadIdx.x; i < (j_b - j_a + 1) * half; i += kThreads) {
+    const int j = small_quotient(i, a.per_half), p = i - j * half, row = j_a + j;
+    const double f = i == static_cast<int>(threadIdx.x) || kThreads % half == 0 ? freq0 : a.freq[p];
+    const double turns = static_cast<double>(t0 + row) * f * 0.15915494309189535;
     const double t = turns - rint(turns);
-    if constexpr (FMT == DSPARK_CACHE_FP4) {
-      double s, c;
-      sincospi(2.0 * t, &s, &c);
-      cs64[row * D + 2 * p] = c;
-      cs64[row * D + 2 * p + 1] = s;
-      cs[row * D + 2 * p] = static_cast<float>(c);
-      cs[row * D + 2 * p + 1] = static_cast<float>(s);
+    float s, c;
+    if (FMT == DSPARK_CACHE_FP4 && row >= k_a && row <= k_b) {
+      double s64, c64;
+      sincospi(2.0 * t, &s64, &c64);
+      cs64[FMT == DSPARK_CACHE_FP4 ? row * D + 2 * p : 0] = c64;
+      cs64[FMT == DSPARK_CACHE_FP4 ? row * D + 2 * p + 1 : 0] = s64;
+      s = static_cast<float>(s64);
+      c = static_cast<float>(c64);
     } else {
-      float s, c;
       sincospif(2.f * static_cast<float>(t), &s, &c);
-      cs[row * D + 2 * p] = c;
-      cs[row * D + 2 * p + 1] = s;
     }
+    cs[row * D + 2 * p] = c;
+    cs[row * D + 2 * p + 1] = s;
   }
   __syncthreads();
 
 #pragma unroll 1
-  for (; u < units; u += gridDim.y * kHeads) {
-    if (u >= n * per_row) {
-      const int v = u - n * per_row;
-      const int h = whole ? v : v % a.Hkv, j = whole ? 0 : v / a.Hkv;
-      const uint16_t* src = a.v + (row_first + j) * a.ldv + static_cast<int64_t>(h) * D + li * 8;
+  for (; u < u_hi; u += kHeads) {
+    if (u >= v0) {
       if (!page) continue;
-      char* head = page + h * PageLayout<FMT, D>::head_bytes(a.P);
+      const int v = u - v0;
       if constexpr (FMT == DSPARK_CACHE_BF16) {
-        char* dst = head + PageLayout<FMT, D>::v(a.P, t8, li * 8);
-        if (whole) store_v8_bf16<D>(src, a.ldv, dst);
-        else store_v1_bf16(src, dst + 2 * (first + j));
+        const int j = whole ? 0 : small_quotient(v, a.per_k), h = v - j * a.Hkv;
+        const uint16_t* src = a.v + (row_first + j) * a.ldv + static_cast<int64_t>(h) * D;
+        char* dst = page + h * PageLayout<FMT, D>::head_bytes(a.P) + PageLayout<FMT, D>::v(a.P, t8, 0);
+        if (whole) store_v8_bf16<D>(src + li * 8, a.ldv, dst + 128 * li);
+        else store_v1_bf16<D>(src, li, dst + 2 * (first + j));
       } else {
-        store_v_fp4<D>(src, a.ldv, li, first, n, head, a.P, t8);
+        const int h = v / kGroup, j = v % kGroup;
+        store_v_fp4<D>(a.v + (row_first + j - first) * a.ldv + static_cast<int64_t>(h) * D + li * 8, li, j, first, n,
+                       page + h * PageLayout<FMT, D>::head_bytes(a.P), a.P, t8);
       }
       continue;
     }
-    const uint16_t* src;
-    const int j = row_of(u, &src), head = u - j * per_row;
-    const bool is_q = head < a.Hq;
+    if (u >= nqk) continue;  // between the keys and V's whole rounds
     const u32x4 now = raw;
-    const int next = u + gridDim.y * kHeads;
-    if (next < n * per_row) {
-      row_of(next, &src);
-      raw = *reinterpret_cast<const u32x4*>(src + li * 8);
-    }
+    if (u + kHeads < min(u_hi, nqk)) raw = *reinterpret_cast<const u32x4*>(source(u + kHeads, row_of(u + kHeads)) + li * 8);
+    const int j = row_of(u);
+    const bool is_q = u < nq;
+    const int head = is_q ? u - j * a.Hq : u - nq - j * a.Hkv;
     if constexpr (FMT == DSPARK_CACHE_FP4) {
       if (!is_q) {
         float f[8];
@@ -311,20 +358,22 @@ __global__ __launch_bounds__(kThreads, 4) void cache_append_kernel(AppendArgs a)
         double x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = f[e];
-        norm_rotate<double, D>(x, li, a.wk, a.eps, a.rot, a.adjacent != 0, cs64 + j * D);
-        if (page)
-          store_k_fp4<D>(x, li, page + (head - a.Hq) * PageLayout<FMT, D>::head_bytes(a.P), a.P, t8 + first + j);
+        norm_rotate<double, D>(x, li, a.wk != nullptr, w_k, a.eps, a.rot, a.adjacent != 0, cs64 + j * D);
+        if (page) store_k_fp4<D>(x, li, page + head * PageLayout<FMT, D>::head_bytes(a.P), a.P, t8 + first + j);
         continue;
       }
     }
     float x[8];
     unpack(now, x);
-    norm_rotate<float, D>(x, li, is_q ? a.wq : a.wk, a.eps, a.rot, a.adjacent != 0, cs + j * D);
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = is_q ? w_q[e] : w_k[e];
+    norm_rotate<float, D>(x, li, is_q ? a.wq != nullptr : a.wk != nullptr, w, a.eps, a.rot, a.adjacent != 0, cs + j * D);
     const u32x4 y = pack_bf16(x);
     if (is_q) {
       *reinterpret_cast<u32x4*>(a.q_out + ((row_first + j) * a.Hq + head) * D + li * 8) = y;
     } else if (page) {
-      char* hp = page + (head - a.Hq) * PageLayout<FMT, D>::head_bytes(a.P);
+      char* hp = page + head * PageLayout<FMT, D>::head_bytes(a.P);
       if constexpr (FMT == DSPARK_CACHE_BF16)
         *reinterpret_cast<u32x4*>(hp + PageLayout<FMT, D>::k(a.P, t8 + first + j, li)) = y;
     }
@@ -413,11 +462,19 @@ hipError_t append_run(AppendArgs& a, hipStream_t s) {
   a.page_bytes = a.Hkv * PageLayout<FMT, D>::head_bytes(a.P);
   a.groups = ceil_div(a.gamma + kGroup, kGroup);  // aligned groups that gamma + 1 tokens can touch
   const int64_t gx = static_cast<int64_t>(a.R) * a.groups;
-  // enough work groups along the heads to fill the device when there are few token groups
-  const int most = ceil_div(kGroup * (a.Hq + a.Hkv) + a.Hkv, kHeads);
-  const int64_t want = 16LL * compute_units() / gx;
+  // a round of head slots a work group where there are few token groups, else
+  // about 12 work groups a compute unit (4 at a time): 128 x 17 packed rows and
+  // 4 x 512 rows take 16.1 and 16.0 us, with 6 a unit 17.2 and 15.6, with 24
+  // 16.6 and 18.6; 32 x 17 rows of 4-bit pages 16.7, 18.7 and 16.6 with their read
+  const int v_units = FMT == DSPARK_CACHE_FP4 ? kGroup * a.Hkv + kGroup - 1 : kGroup * a.Hkv;
+  const int most = ceil_div(kGroup * (a.Hq + a.Hkv) + v_units, kHeads);
+  const int64_t want = 12LL * compute_units() / gx;
   const int gy = want < 1 ? 1 : want > most ? most : static_cast<int>(want);
-  cache_append_kernel<FMT, D><<<dim3(static_cast<unsigned>(gx), gy), kThreads, 0, s>>>(a);
+  a.page_shift = __builtin_ctz(a.P);
+  a.per_q = 1.f / a.Hq;
+  a.per_k = 1.f / a.Hkv;
+  a.per_half = a.rot > 0 ? 2.f / a.rot : 0.f;
+  cache_append_kernel<FMT, D><<<dim3(a.groups, gy, a.R), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -450,7 +507,8 @@ hipError_t cache_append_launch(int fmt, int R, int gamma, int Hq, int Hkv, int D
   AppendArgs a{R, gamma, Hq, Hkv, P, n_pages, max_pages, 0,
                static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                ldq, ldk, ldv, static_cast<const uint16_t*>(wq), static_cast<const uint16_t*>(wk), eps, freq, rot,
-               adjacent, row0, ell, len, table, static_cast<uint16_t*>(q_out), static_cast<char*>(pool), 0};
+               adjacent, row0, ell, len, table, static_cast<uint16_t*>(q_out), static_cast<char*>(pool), 0, 0, 0.f,
+               0.f, 0.f};
   return fmt == DSPARK_CACHE_BF16 ? append_d<DSPARK_CACHE_BF16>(D, a, s) : append_d<DSPARK_CACHE_FP4>(D, a, s);
 }
 
