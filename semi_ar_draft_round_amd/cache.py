@@ -10,9 +10,10 @@ and calls the entry points in the order a round needs:
         o, _ = cache.attend(layer, q, ...)
     cache.commit(d.n_acc)                         # after dspark_verify
 
-Nothing is allocated after construction except output tensors that the
-caller does not pass, so a round can be captured in a HIP graph.  All calls
-run on the current stream.
+Nothing is allocated after construction except output tensors and the
+attention's workspace where the caller does not pass them, from torch's
+allocator, so a round can be captured in a HIP graph.  All calls run on the
+current stream.
 """
 
 from __future__ import annotations
