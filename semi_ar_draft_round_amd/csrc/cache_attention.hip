@@ -12,15 +12,27 @@
 //                  each 16 into half h of the wave, which is where the B
 //                  operand wants them, and V lies in the pages with a dim's 8
 //                  tokens together, which is the A operand.
-// Nothing goes through LDS on the way: pages hold both operands in 16-byte
-// pieces, contiguous over the lanes that read them.
+// Pages hold both operands in 16-byte pieces, contiguous over the lanes that
+// read them, so a tile goes straight into registers where every wave has
+// tiles of its own (rows of one row tile; 4 bits), and past the registers into
+// a ring in LDS where several waves multiply the same 16-bit tile.
 //
 // Work is split over tokens as well as rows.  The units (request, row block,
-// head, tile) are numbered in that order, and every work group takes an equal
-// contiguous run of them, whatever the requests' lengths.  A (request, row
-// block, head) that lies in one run is finished there; of one that crosses
-// runs, every part leaves (max, sum, unnormalised output) in the workspace,
-// and a second launch joins them in order.
+// head, tile) are numbered in that order, and every work group takes a
+// contiguous run of them, whatever the requests' lengths, or a whole part of a
+// head where heads are few and of one length.  A (request, row block, head)
+// that lies in one run is finished there; of one that crosses runs, every part
+// leaves (max, sum, unnormalised output) in the workspace, and a second launch
+// joins them in order.
+//
+// What bounds it, with 8 heads of 128 dims: the pages' bytes for 16 bits (128
+// requests of up to 17 rows x 7 query heads a head, ragged contexts up to
+// 8192: 536 us, 4.9 TB/s; one request x 17 rows over 131072 tokens 118 us, 4.6
+// TB/s) and for single tokens of 4 bits (32 requests over 16384 tokens 89 us,
+// 4.0 TB/s); the vector units for many rows of 4 bits (the same 128 requests
+// up to 16384 tokens 419 us, two fifths of it the exponentials and their
+// sums); and for short contexts the two launches and the chain of loads before
+// the first tile, 6 of 13 us (one token over 1023).
 #include "cache.hpp"
 
 namespace dspark {
@@ -317,18 +329,50 @@ __device__ __forceinline__ void add_non_finite(f32x16 (&o)[D / 32], const float 
 // What starting another head costs a work group, in units (5 us of them).
 constexpr int kRestart = 16;
 
-// Tiles of a part of a head in `parts` parts, the last ones perhaps empty.
-__device__ __forceinline__ int part_tiles(int count, int weight, int parts) {
-  return max((count + parts - 1) / parts, (kMinUnits + weight - 1) / weight);
-}
+// Of two work groups on a compute unit the one that came first is served
+// first.  Where the vector units set the pace (4-bit heads of 64 and 128 dims)
+// it is through with an equal share after 421 us when the other takes 499
+// (128 requests x 17 rows over 8192 tokens), so it gets more, in 64ths of an
+// equal share: 454 -> 446 us over ragged contexts up to 16384, 132 -> 125 us
+// for 32 requests over 8192 (4 and 10 of 64: 457 and 454, 125 and 124).  At
+// the pace of memory it makes no difference (16-bit pages: 545 and 539 us,
+// 254 and 254 us), and short runs lose: only from 4 kMinUnits a work group on.
+constexpr int kFavour = 7;
 
-// The range of units of work group wg: `share` each, the first `rest` one more.
+// A head in `parts` parts of `tiles` tiles, the last ones perhaps empty; with
+// `more` > 0 parts come in pairs, the first of a pair that much longer.
+template <bool FAVOURED>
+struct Parts {
+  int count, tiles, more;
+  __device__ __forceinline__ Parts(int count, int weight, int parts, bool paired)
+      : count(count), tiles(max((count + parts - 1) / parts, (kMinUnits + weight - 1) / weight)),
+        more(FAVOURED && paired ? tiles * kFavour / 64 : 0) {}
+  __device__ __forceinline__ int begin(int j) const {
+    return static_cast<int>(min(static_cast<int64_t>(j) * tiles + (FAVOURED ? (j & 1) * more : 0),
+                                static_cast<int64_t>(count)));
+  }
+  // those that are not empty
+  __device__ __forceinline__ int used() const {
+    const int n = (count + tiles - 1) / tiles;
+    return FAVOURED && begin(n - 1) == count ? n - 1 : n;
+  }
+};
+
+// The range of units of work group wg: `first` for each of the first n,
+// `share` for the others, of which the first `rest` get one more.
+template <bool FAVOURED>
 struct Deal {
-  int64_t share, rest;
-  __device__ __forceinline__ int64_t begin(int64_t wg) const { return share * wg + (wg < rest ? wg : rest); }
+  int64_t share, rest, first;
+  int n;
+  __device__ __forceinline__ int64_t begin(int wg) const {
+    if (FAVOURED && wg < n) return wg * first;
+    const int64_t x = FAVOURED ? wg - n : wg;
+    return (FAVOURED ? n * first : 0) + share * x + (x < rest ? x : rest);
+  }
   __device__ __forceinline__ int owner(int64_t unit) const {
-    const int64_t big = rest * (share + 1);
-    return static_cast<int>(unit < big ? quotient(unit, share + 1) : rest + quotient(unit - big, share));
+    if (FAVOURED && unit < n * first) return static_cast<int>(quotient(unit, first));
+    const int64_t x = FAVOURED ? unit - n * first : unit, big = rest * (share + 1);
+    return static_cast<int>((FAVOURED ? n : 0) + (x < big ? quotient(x, share + 1) : rest + quotient(x - big, share)));
   }
 };
 
@@ -391,21 +435,23 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   const int per = ceil_div(entries, T);
   const int e0 = min(entries, static_cast<int>(threadIdx.x) * per), e1 = min(entries, e0 + per);
   if (threadIdx.x == 0) lds_run[0] = lds_run[1] = 0;
-  Deal deal{0, 0};
+  constexpr bool kFavoured = FMT == DSPARK_CACHE_FP4 && D != 256;
+  Deal<kFavoured> deal{0, 0, 0, 0};
   int64_t at = 0, u0 = 0;
   int nb = 0, parts = 0;  // parts of a head; 0: equal runs
   int heads_at = 0, my_head = 0, my_part = 0;
+  int place_of = wg;  // its slots in the workspace: in the order of a head's parts
+  bool paired = false;
   auto place = [&](int e, int64_t units_at, int first_head, int count, int weight) {
     const int64_t per_head = static_cast<int64_t>(count) * weight;
     if (parts > 0) {
       const int x = my_head - first_head;
       if (count == 0 || x < 0 || x >= a.Hkv) return;
-      const int c = part_tiles(count, weight, parts);
+      const Parts<kFavoured> split(count, weight, parts, paired);
       lds_entry = e;
       lds_base = units_at;
-      lds_run[0] = units_at + x * per_head + min(static_cast<int64_t>(my_part) * c, static_cast<int64_t>(count)) * weight;
-      lds_run[1] =
-          units_at + x * per_head + min((my_part + 1) * static_cast<int64_t>(c), static_cast<int64_t>(count)) * weight;
+      lds_run[0] = units_at + x * per_head + static_cast<int64_t>(split.begin(my_part)) * weight;
+      lds_run[1] = units_at + x * per_head + static_cast<int64_t>(split.begin(my_part + 1)) * weight;
     } else if (u0 >= units_at && u0 < units_at + per_head * a.Hkv) {
       lds_entry = e;
       lds_base = units_at;
@@ -461,15 +507,26 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       heads_at = heads_before + heads_incl - heads;
       const int64_t useful = N / kMinUnits;
       nb = useful < 1 ? 1 : useful < gridDim.x ? static_cast<int>(useful) : static_cast<int>(gridDim.x);
-      deal.share = quotient(N, nb);
-      deal.rest = N - deal.share * nb;
+      const int64_t equal = quotient(N, nb);
+      deal.share = equal;
+      deal.rest = N - equal * nb;
+      if (kFavoured && nb == static_cast<int>(gridDim.x) && equal >= 4 * kMinUnits) {
+        deal.n = nb / 2;
+        deal.first = equal + equal * kFavour / 64;
+        const int64_t others = N - deal.n * deal.first;
+        deal.share = quotient(others, nb - deal.n);
+        deal.rest = others - deal.share * (nb - deal.n);
+      }
       u0 = deal.begin(wg);
       if (H > 0 && H <= static_cast<int>(gridDim.x)) {
         const int p = min(static_cast<int>(gridDim.x / H), ceil_div(longest, kMinUnits));
-        if (longest / p <= deal.share + kRestart) {
+        if (longest / p <= equal + kRestart) {
+          const int half = gridDim.x / 2;
           parts = p;
-          my_head = wg / p;
-          my_part = wg - my_head * p;
+          paired = kFavoured && (p & 1) == 0 && H * p > half && longest / p >= 4 * kMinUnits;
+          if (paired) place_of = wg < half ? 2 * wg : 2 * (wg - half) + 1;
+          my_head = place_of / p;
+          my_part = place_of - my_head * p;
         }
       }
       if (per == 1 && e0 < e1) place(e0, at, heads_at, count, weight);
@@ -574,8 +631,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       else return q_reg[x];
     };
 
-    // One tile: its scores s, its values, first token ct and pages c0, c1.
-    auto absorb = [&](f32x16 s, VTile<FMT, D>& vt, int ct, int c0, int c1, bool clear) {
+    // One tile: its scores s, its values, first token ct and pages c0, c1;
+    // ahead(): what may run beside the exponentials.
+    auto absorb = [&](f32x16 s, VTile<FMT, D>& vt, int ct, int c0, int c1, bool clear, auto ahead) {
       if (!clear) {
         rare();
 #pragma unroll
@@ -602,6 +660,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 #pragma unroll
           for (int j = 0; j < 16; ++j) acc.o[x][j] *= keep;
       }
+      ahead();
       float p[16], sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -727,13 +786,17 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
             for (int x = 0; x < NB; ++x) vt.x[s2][x] = tile[(KS + s2 * NB + x) * 64];
           const int c0 = __builtin_amdgcn_readlane(own.v0, round & 63);
           const int c1 = TWO ? __builtin_amdgcn_readlane(own.v1, round & 63) : c0;
-          absorb(s, vt, token_at(t), c0, c1, (clear_v >> (round & 63)) & 1u);
+          absorb(s, vt, token_at(t), c0, c1, (clear_v >> (round & 63)) & 1u, [] {});
         }
       }
       wait_and_meet<0>();
     }
     if constexpr (D != 256 || !kShared) if (!shared && active && wt < tiles) {
-      // Every wave for itself, straight into registers, a tile ahead.
+      // Every wave for itself, straight into registers, a tile ahead.  4-bit
+      // tiles leave room for the next one's scores, whose products then run
+      // beside this one's exponentials (128 requests x up to 17 rows over
+      // ragged contexts up to 16384: 452 -> 419 us with it).
+      constexpr bool kAhead = FMT == DSPARK_CACHE_FP4 && !kQueryInLds;
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
       KTile<FMT, D> kt;
@@ -753,29 +816,58 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       auto load_k = [&]() {
         kt.load(head_of(TWO && col >= 16 ? id1 : id0), TWO ? 16 : a.P, TWO ? 0 : tok & (a.P - 1), k_lane, k_token);
       };
-      auto load_v = [&]() {
+      auto load_v = [&](VTile<FMT, D>& v) {
         const int t = TWO ? 0 : tok & (a.P - 1);
-        vt.load(0, head_of(id0), TWO ? 16 : a.P, t, v_lane, h);
-        vt.load(1, head_of(id1), TWO ? 16 : a.P, TWO ? 0 : t + 16, v_lane, h);
+        v.load(0, head_of(id0), TWO ? 16 : a.P, t, v_lane, h);
+        v.load(1, head_of(id1), TWO ? 16 : a.P, TWO ? 0 : t + 16, v_lane, h);
       };
       fetch(0);
       aim(0);
       load_k();
-      load_v();
-#pragma unroll 1
-      for (int k = 0; k < steps; ++k) {
-        const f32x16 s = kt.scores(q, h);
-        const int c0 = id0, c1 = id1, ct = tok;
-        const bool clear = (clear_v >> (k & 63)) & 1u;
-        // the next tile's keys (after the last tile: its own again, unused)
-        if ((k & 63) == 63 && k + 1 < steps) {
+      // tile k, or after the last tile that one again (loaded, not used)
+      auto next = [&](int k) {
+        if ((k & 63) == 0 && k < steps) {
           rare();
-          fetch(k + 1);
+          fetch(k);
         }
-        aim(min(k + 1, steps - 1));
+        aim(min(k, steps - 1));
+      };
+      if constexpr (!kAhead) {
+        load_v(vt);
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k) {
+          const f32x16 s = kt.scores(q, h);
+          const int c0 = id0, c1 = id1, ct = tok;
+          const bool clear = (clear_v >> (k & 63)) & 1u;
+          next(k + 1);
+          load_k();
+          absorb(s, vt, ct, c0, c1, clear, [] {});
+          load_v(vt);
+        }
+      } else {
+        VTile<FMT, D> vu;
+        load_v(vt);
+        f32x16 s = kt.scores(q, h);
+        int c0 = id0, c1 = id1, ct = tok;
+        bool clear = clear_v & 1u;
+        next(1);
         load_k();
-        absorb(s, vt, ct, c0, c1, clear);
-        load_v();
+        // tile k with its scores in s, values in `now`; kt has the next one's keys
+        auto turn = [&](VTile<FMT, D>& now, VTile<FMT, D>& then, int k) {
+          load_v(then);
+          f32x16 ahead;
+          absorb(s, now, ct, c0, c1, clear, [&] { ahead = kt.scores(q, h); });
+          s = ahead;
+          c0 = id0, c1 = id1, ct = tok;
+          clear = (clear_v >> ((k + 1) & 63)) & 1u;
+          next(k + 2);
+          load_k();
+        };
+#pragma unroll 1
+        for (int k = 0; k < steps; k += 2) {
+          turn(vt, vu, k);
+          if (k + 1 < steps) turn(vu, vt, k + 1);
+        }
       }
     }
 
@@ -783,7 +875,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
     // in LDS and takes an equal share of its rows' dims from all of them.
     const bool opens = t0 == 0, closes = t1 == b.count;
     const bool valid = wq * kTile + col < b.rows;
-    const int64_t slot = (static_cast<int64_t>(wg) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
+    const int64_t slot = (static_cast<int64_t>(place_of) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
     if (active) lds_ml[wave][lane] = make_float2(acc.m, acc.l);
     __syncthreads();
     const bool whole = opens && closes;
@@ -835,9 +927,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
     __syncthreads();  // before the next segment's waves write there
     if (opens) {  // the work group that holds the last tile's first unit has the last part
       const int n = closes ? 0
-                    : parts > 0 ? ceil_div(b.count, part_tiles(b.count, weight, parts))
+                    : parts > 0 ? Parts<kFavoured>(b.count, weight, parts, paired).used()
                                 : deal.owner(seg_end - weight) - wg + 1;
-      left = Desc{n, b.rows, b.m0, hk, first_row, wg, 0};
+      left = Desc{n, b.rows, b.m0, hk, first_row, place_of, 0};
       if (a.by_head && threadIdx.x == 0) reinterpret_cast<Desc*>(a.desc)[entry * a.Hkv + hk] = left;
     }
   }

@@ -317,3 +317,75 @@ def test_streams_graphs_and_repeats(fmt, dev):
         torch.cuda.synchronize()
         same(a, outs[0])
         same(b, outs[1])
+
+
+LARGE = [  # lens, ells, Hq, Hkv, D, P, gamma: how the work is dealt
+    ([40_000, 9_001, 33, 25_000, 17_000], [16, 3, 0, 16, 9], 16, 8, 64, 64, 16),  # equal runs whatever the requests
+    ([16_383] * 8, [0] * 8, 16, 8, 128, 64, 0),               # whole parts of heads, an even number
+    ([12_000, 11_990, 12_011], [5, 5, 5], 8, 8, 128, 16, 5),  # an odd number
+    ([6_000] * 8, [16] * 8, 32, 8, 64, 128, 16),              # four row tiles a head
+    ([3_000, 10, 2_500], [-1, 16, -1], 4, 2, 128, 32, 16),    # few heads, most requests idle
+    ([2_000] * 6, [16] * 6, 8, 2, 256, 64, 16),
+    (list(range(40)) * 103, [0, -1, 0] * 1373, 2, 1, 64, 16, 0),                  # 4096 requests at most: 4119 cut below
+]
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP4])
+@pytest.mark.parametrize("case", LARGE, ids=["runs", "parts", "odd-parts", "row-tiles", "idle", "d256", "r4096"])
+def test_work_shared_out(case, fmt, dev):
+    """Batches large enough for every way of dealing the work out, against
+    float64 on the device over the values that dspark_cache_read gives (of
+    4 bits V rounded to bf16, which adds 2^-8 of sum_j p_j |v_j|)."""
+    from semi_ar_draft_round_amd import binding as B
+    lens, ells, Hq, Hkv, D, P, gamma = case
+    lens, ells = lens[:4096], ells[:4096]
+    say(f"[attention] {len(lens)} requests, fmt {fmt}, D {D}")
+    R, T = len(lens), max(lens) + gamma + 1
+    g = torch.Generator(device=dev).manual_seed(17)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+    mp = -(-T // P)
+    pool = torch.full((R * mp, B.dspark_cache_page_bytes(fmt, Hkv, D, P)), 0xFF, dtype=torch.uint8, device=dev)
+    table = torch.randperm(R * mp, generator=g, device=dev).to(torch.int32).view(R, mp)
+    total = [n + max(e, -1) + 1 for n, e in zip(lens, ells)]
+    C = min(1024, T)
+    for at in range(0, T, C):
+        x = torch.randn((R * C, 1 + 2 * Hkv, D), generator=g, device=dev).to(torch.bfloat16)
+        B.dspark_cache_append(x[:, :1], x[:, 1:1 + Hkv], x[:, 1 + Hkv:], pool, table, i32([min(at, t) for t in total]),
+                              i32([min(t - at, C) - 1 if t > at else -1 for t in total]), C - 1, fmt=fmt, page=P)
+    n = [e + 1 for e in ells]
+    first = np.cumsum([0] + n)[:-1].tolist()
+    q = torch.randn((sum(n), Hq, D), generator=g, device=dev).to(torch.bfloat16)
+    lse = torch.zeros((sum(n), Hq), device=dev)
+    out, _ = B.dspark_cache_attention(q, pool, table, i32(lens), i32(ells), gamma, fmt=fmt, page=P, heads_kv=Hkv,
+                                      row0=i32(first), lse=lse)
+    again, _ = B.dspark_cache_attention(q, pool, table, i32(lens), i32(ells), gamma, fmt=fmt, page=P, heads_kv=Hkv,
+                                        row0=i32(first))
+    assert torch.equal(out, again)
+    scale, worst = D ** -0.5, 0.0
+    for r in range(R):
+        if n[r] == 0 or (R > 100 and r % 7):
+            continue
+        N = total[r]
+        k, v = B.dspark_cache_read(pool, table[r:r + 1].contiguous(), None, i32([N]), N, fmt=fmt, page=P, heads_kv=Hkv,
+                                   dim=D)
+        k, v = (y[0].double().permute(1, 0, 2).contiguous() for y in (k, v))
+        mine = slice(first[r], first[r] + n[r])
+        x = q[mine].double().view(n[r], Hkv, -1, D).permute(1, 0, 2, 3).reshape(Hkv, -1, D)
+        s = (torch.bmm(x, k.transpose(1, 2).contiguous()) * scale).view(Hkv, n[r], -1, N)
+        for i in range(n[r]):
+            s[:, i, :, lens[r] + i + 1:] = float("-inf")
+        z = torch.logsumexp(s, -1)
+        p = torch.exp(s - z[..., None]).view(Hkv, -1, N)
+        rows = lambda y: y.view(Hkv, n[r], -1, D).permute(1, 0, 2, 3).reshape(n[r], Hq, D)
+        want, mean_abs = rows(torch.bmm(p, v)), rows(torch.bmm(p, v.abs().contiguous()))
+        # as attention_tolerance, sum |q k| at most the product of the norms
+        delta = 2 * (D + 8) * 2.0 ** -24 * float(x.norm(dim=-1).max() * k.norm(dim=-1).max()) * scale
+        rest = delta + (N + 64) * 2.0 ** -24
+        half = 2.0 ** -8
+        tol = half * want.abs() + (half * (1 + half) + rest + (half if fmt == FP4 else 0)) * mean_abs + 1e-30
+        err = (out[mine].double() - want).abs()
+        assert bool((err <= tol).all()), (r, float((err / tol).max()))
+        worst = max(worst, float((err / tol).max()))
+        zr = z.permute(1, 0, 2).reshape(n[r], Hq)
+        assert bool(((lse[mine].double() - zr).abs() <= rest + 1e-6 + 2.0 ** -22 * zr.abs()).all())
+    say(f"  worst error {worst:.3f} of its bound")
