@@ -113,9 +113,9 @@ size_t dspark_cache_workspace_size(dspark_cache_ws_kind kind, int R, int gamma, 
  *   pool   out: pages of format fmt
  *
  * Limits: 1 <= R <= 4096, 0 <= gamma <= 1023, 1 <= Hq <= 1024, 1 <= n_pages
- * <= 2^20, 1 <= max_pages <= 2^20, rows of one request below 2^31.  Two rows
- * never fall on one token unless two requests' tables name one page for it:
- * reserve sees to that.
+ * <= 2^20, 1 <= max_pages <= 2^20, R * max_pages < 2^31, len[r] <= 2^29 (past
+ * every table: 2^20 pages of 128 tokens).  Two rows never fall on one token
+ * unless two requests' tables name one page for it: reserve sees to that.
  */
 dspark_status dspark_cache_append(int fmt, int R, int gamma, int Hq, int Hkv, int D, int P, int n_pages,
                                   int max_pages, const void* q, int64_t ldq, const void* k, int64_t ldk,
@@ -144,7 +144,7 @@ dspark_status dspark_cache_append(int fmt, int R, int gamma, int Hq, int Hkv, in
  *   lse  [rows][Hq] f32 out, or NULL
  *   window >= 0, sinks >= 0 (ignored without a window)
  *   ws   dspark_cache_workspace_size(DSPARK_CACHE_WS_ATTENTION, R, gamma, Hq,
- *        Hkv, D) bytes; contents on entry are irrelevant
+ *        Hkv, D) bytes, 16-byte aligned; contents on entry are irrelevant
  *
  * Limits: as append; Hq a multiple of Hkv; scale finite.
  */
@@ -162,7 +162,7 @@ dspark_status dspark_cache_attention(int fmt, int R, int gamma, int Hq, int Hkv,
  * ([Hkv][D]); other rows are left as they were, tokens without a page read as
  * zero.  4-bit values are exact in bf16 for K, and rounded once for V.
  *
- *   start NULL: 0.  Limits: as append; 1 <= T, R * T < 2^31.
+ *   start NULL: 0.  Limits: as append; 1 <= T <= 2^26.
  */
 dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, int n_pages, int max_pages,
                                 const int32_t* start, const int32_t* count, const int32_t* table, const void* pool,

@@ -17,6 +17,7 @@ constexpr int kCacheMaxR = 4096;
 constexpr int kCacheMaxGamma = 1023;
 constexpr int kCacheMaxHeads = 1024;
 constexpr int kCacheMaxPages = 1 << 20;
+constexpr int kCacheMaxT = 1 << 26;  // rows of a read: its grid stays below 2^32 threads
 
 // Byte offsets inside one head's part of a page (dspark_cache.h, Pages).
 template <int FMT, int D>

@@ -15,7 +15,7 @@ hipError_t cache_read_launch(int fmt, int R, int T, int Hkv, int D, int P, int n
                              const int32_t* start, const int32_t* count, const int32_t* table, const void* pool,
                              void* k, void* v, hipStream_t s);
 // cache_attention.hip
-size_t cache_attention_workspace_bytes(int R, int gamma, int Hq, int Hkv, int D);
+size_t cache_attention_workspace_bytes(int gamma, int Hq, int Hkv, int D);
 hipError_t cache_attention_launch(int fmt, int R, int gamma, int Hq, int Hkv, int D, int P, int n_pages,
                                   int max_pages, const void* q, float scale, int window, int sinks,
                                   const int32_t* row0, const int32_t* ell, const int32_t* len, const int32_t* table,
@@ -75,7 +75,7 @@ size_t dspark_cache_workspace_size(dspark_cache_ws_kind kind, int R, int gamma, 
   switch (kind) {
     case DSPARK_CACHE_WS_ATTENTION:
       if (!batch_ok(R, gamma) || !heads_ok(a) || !heads_ok(b) || a % b != 0 || !dim_ok(c)) return 0;
-      return round256(cache_attention_workspace_bytes(R, gamma, a, b, c));
+      return round256(cache_attention_workspace_bytes(gamma, a, b, c));
     case DSPARK_CACHE_WS_RESERVE:  // the ids handed out
       if (!pages_ok(R, b, a)) return 0;
       return round256(4 * static_cast<size_t>(b));
@@ -127,9 +127,10 @@ dspark_status dspark_cache_attention(int fmt, int R, int gamma, int Hq, int Hkv,
     return DSPARK_EINVAL;
   if (window < 0 || sinks < 0 || !isfinite(scale)) return DSPARK_EINVAL;
   if (!q || !ell || !len || !table || !pool || !out) return DSPARK_EINVAL;
-  if (!aligned(static_cast<const char*>(q), static_cast<const char*>(pool), static_cast<const char*>(out)))
+  if (!aligned(static_cast<const char*>(q), static_cast<const char*>(pool), static_cast<const char*>(out),
+               static_cast<const char*>(ws)))
     return DSPARK_EINVAL;
-  if (!ws || ws_bytes < round256(cache_attention_workspace_bytes(R, gamma, Hq, Hkv, D))) return DSPARK_EWORKSPACE;
+  if (!ws || ws_bytes < round256(cache_attention_workspace_bytes(gamma, Hq, Hkv, D))) return DSPARK_EWORKSPACE;
   dspark_status st = check_device();
   if (st != DSPARK_OK) return st;
   return launched(cache_attention_launch(fmt, R, gamma, Hq, Hkv, D, P, n_pages, max_pages, q, scale, window, sinks,
@@ -141,8 +142,7 @@ dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, in
                                 const int32_t* start, const int32_t* count, const int32_t* table, const void* pool,
                                 void* k, void* v, void* stream) {
   if (!format_ok(fmt)) return DSPARK_EDTYPE;
-  if (!heads_ok(Hkv) || !dim_ok(D) || !page_ok(P) || !pages_ok(R, n_pages, max_pages) || T < 1 ||
-      static_cast<int64_t>(R) * T >= (1LL << 31))
+  if (!heads_ok(Hkv) || !dim_ok(D) || !page_ok(P) || !pages_ok(R, n_pages, max_pages) || T < 1 || T > kCacheMaxT)
     return DSPARK_EINVAL;
   if (!count || !table || !pool || !k || !v) return DSPARK_EINVAL;
   if (!aligned(static_cast<const char*>(pool), static_cast<const char*>(k), static_cast<const char*>(v)))

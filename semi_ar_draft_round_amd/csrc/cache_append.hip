@@ -381,7 +381,7 @@ __global__ __launch_bounds__(kThreads, 4) void cache_append_kernel(AppendArgs a)
 }
 
 struct ReadArgs {
-  int R, T, Hkv, P, n_pages, max_pages, groups;
+  int R, T, Hkv, P, n_pages, max_pages;
   const int32_t *start, *count, *table;
   const char* pool;
   int64_t page_bytes;
@@ -394,7 +394,7 @@ template <int FMT, int D>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadArgs a) {
   typedef PageLayout<FMT, D> PL;
   constexpr int L = D / 8, kHeads = kThreads / L;
-  const int r = blockIdx.x / a.groups, g = blockIdx.x % a.groups;
+  const int r = blockIdx.z, g = blockIdx.x;
   const int64_t start = a.start ? a.start[r] : 0;
   const int n_rows = min(max(a.count[r], 0), a.T);
   if (start < 0) return;
@@ -482,9 +482,8 @@ template <int FMT, int D>
 hipError_t read_run(ReadArgs& a, hipStream_t s) {
   constexpr int kHeads = kThreads / (D / 8);
   a.page_bytes = a.Hkv * PageLayout<FMT, D>::head_bytes(a.P);
-  a.groups = ceil_div(a.T - 1 + kGroup, kGroup);
-  const int64_t gx = static_cast<int64_t>(a.R) * a.groups;
-  cache_read_kernel<FMT, D><<<dim3(static_cast<unsigned>(gx), ceil_div(2 * a.Hkv, kHeads)), kThreads, 0, s>>>(a);
+  const int groups = ceil_div(a.T - 1 + kGroup, kGroup);
+  cache_read_kernel<FMT, D><<<dim3(groups, ceil_div(2 * a.Hkv, kHeads), a.R), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -515,7 +514,7 @@ hipError_t cache_append_launch(int fmt, int R, int gamma, int Hq, int Hkv, int D
 hipError_t cache_read_launch(int fmt, int R, int T, int Hkv, int D, int P, int n_pages, int max_pages,
                              const int32_t* start, const int32_t* count, const int32_t* table, const void* pool,
                              void* k, void* v, hipStream_t s) {
-  ReadArgs a{R, T, Hkv, P, n_pages, max_pages, 0, start, count, table, static_cast<const char*>(pool), 0,
+  ReadArgs a{R, T, Hkv, P, n_pages, max_pages, start, count, table, static_cast<const char*>(pool), 0,
              static_cast<uint16_t*>(k), static_cast<uint16_t*>(v)};
   return fmt == DSPARK_CACHE_BF16 ? read_d<DSPARK_CACHE_BF16>(D, a, s) : read_d<DSPARK_CACHE_FP4>(D, a, s);
 }

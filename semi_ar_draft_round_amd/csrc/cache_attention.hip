@@ -72,7 +72,6 @@ struct Desc {
   int head;
   int64_t first_row;  // the request's row 0 in q and out
   int wg;
-  int pad;
 };
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 x) {
@@ -929,7 +928,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       const int n = closes ? 0
                     : parts > 0 ? Parts<kFavoured>(b.count, weight, parts, paired).used()
                                 : deal.owner(seg_end - weight) - wg + 1;
-      left = Desc{n, b.rows, b.m0, hk, first_row, place_of, 0};
+      left = Desc{n, b.rows, b.m0, hk, first_row, place_of};
       if (a.by_head && threadIdx.x == 0) reinterpret_cast<Desc*>(a.desc)[entry * a.Hkv + hk] = left;
     }
   }
@@ -1064,8 +1063,7 @@ hipError_t run_d(int D, AttnArgs& a, void* ws, hipStream_t s) {
 
 }  // namespace
 
-size_t cache_attention_workspace_bytes(int R, int gamma, int Hq, int Hkv, int D) {
-  (void)R;
+size_t cache_attention_workspace_bytes(int gamma, int Hq, int Hkv, int D) {
   // sized for the largest grid: the size does not depend on the device
   const size_t grid = D == 256 ? kMaxGrid / 2 : kMaxGrid;
   const size_t rows = grid * 2 * slot_tiles_of(gamma, Hq, Hkv) * kTile;

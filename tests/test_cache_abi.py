@@ -92,7 +92,7 @@ def test_attention_refusals(lib):
     assert call(fmt=7) == EDTYPE
     for bad in (dict(R=0), dict(gamma=1024), dict(Hq=9), dict(D=80), dict(page=0), dict(n_pages=0), dict(mp=0),
                 dict(window=-1), dict(sinks=-1), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None),
-                dict(ptr=None), dict(out=None), dict(q=ODD), dict(out=ODD)):
+                dict(ptr=None), dict(out=None), dict(q=ODD), dict(out=ODD), dict(ws=ODD)):
         assert call(**bad) == EINVAL, bad
     assert call(ws=None) == EWORKSPACE
     assert call(n=16) == EWORKSPACE
@@ -102,7 +102,7 @@ def test_read_refusals(lib):
     def call(fmt=1, R=4, T=3, Hkv=2, D=128, page=64, n_pages=50, mp=4, ptr=FAKE, pool=FAKE):
         return lib.dspark_cache_read(fmt, R, T, Hkv, D, page, n_pages, mp, None, ptr, ptr, pool, ptr, ptr, None)
     assert call(fmt=0) == EDTYPE
-    for bad in (dict(R=0), dict(T=0), dict(T=1 << 29), dict(Hkv=0), dict(D=1), dict(page=1), dict(n_pages=0), dict(mp=0),
+    for bad in (dict(R=0), dict(T=0), dict(T=(1 << 26) + 1), dict(T=1 << 29), dict(Hkv=0), dict(D=1), dict(page=1), dict(n_pages=0), dict(mp=0),
                 dict(ptr=None), dict(pool=ODD)):
         assert call(**bad) == EINVAL, bad
 
