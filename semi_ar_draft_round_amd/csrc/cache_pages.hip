@@ -276,6 +276,51 @@ __global__ __launch_bounds__(256) void cache_fork_drop(int R, int n_pages, int m
   if (threadIdx.x == 0) len[r] = s < 0 ? 0 : new_len[r];
 }
 
+// Both in one launch of one work group for tables of at most 4 kT entries,
+// a thread's four in registers: a round's bookkeeping (fork, reserve, copy,
+// commit) of 128 requests x 18 pages takes the GPU 23.2 us with it and 22.8
+// with two launches, and the host 35.5 us instead of 38.7.
+constexpr int kForkPer = 4;
+__global__ __launch_bounds__(kT) void cache_fork_small(int R, int P, int n_pages, int max_pages, const int32_t* from,
+                                                       int32_t* len, int32_t* table, int32_t* ref, uint32_t* bits) {
+  const int n = R * max_pages;
+  int id[kForkPer], old[kForkPer], new_len[kForkPer];
+  bool mine[kForkPer];
+#pragma unroll
+  for (int j = 0; j < kForkPer; ++j) {
+    const int e = j * kT + threadIdx.x;
+    mine[j] = e < n;
+    id[j] = old[j] = -1;
+    new_len[j] = 0;
+    if (!mine[j]) continue;
+    const int r = e / max_pages, i = e - r * max_pages, s = fork_source(r, R, from);
+    mine[j] = s != r;
+    if (s == r) continue;
+    old[j] = page_or_none(table[e], n_pages);
+    if (s < 0) continue;
+    new_len[j] = len[s];
+    const int64_t pages = (static_cast<int64_t>(max(new_len[j], 0)) + P - 1) / P;
+    if (i < pages) id[j] = page_or_none(table[s * max_pages + i], n_pages);
+  }
+#pragma unroll
+  for (int j = 0; j < kForkPer; ++j)
+    if (id[j] >= 0) atomicAdd(&ref[id[j]], 1);
+  // all increments before all decrements, all reads before all writes; one
+  // work group, so its barrier orders them
+  __syncthreads();
+  int was[kForkPer];
+#pragma unroll
+  for (int j = 0; j < kForkPer; ++j) was[j] = old[j] >= 0 ? atomicSub(&ref[old[j]], 1) : 0;
+#pragma unroll
+  for (int j = 0; j < kForkPer; ++j)
+    if (mine[j]) {
+      const int e = j * kT + threadIdx.x;
+      if (was[j] == 1) atomicOr(&bits[old[j] >> 5], 1u << (old[j] & 31));
+      table[e] = id[j];
+      if (e % max_pages == 0) len[e / max_pages] = new_len[j];
+    }
+}
+
 // ws: word 0 = U, then the new id of every page that moves.
 __global__ __launch_bounds__(kT) void cache_compact_plan(int n_pages, uint32_t* bits, int32_t* pairs,
                                                          int32_t* n_pairs, int32_t* used, int32_t* map) {
@@ -388,6 +433,10 @@ hipError_t cache_commit_launch(int R, int gamma, int P, int n_pages, int max_pag
 
 hipError_t cache_fork_launch(int R, int P, int n_pages, int max_pages, const int32_t* from, int32_t* len,
                              int32_t* table, int32_t* ref, uint32_t* bits, void* ws, hipStream_t s) {
+  if (static_cast<int64_t>(R) * max_pages <= kForkPer * kT) {
+    cache_fork_small<<<1, kT, 0, s>>>(R, P, n_pages, max_pages, from, len, table, ref, bits);
+    return hipGetLastError();
+  }
   int32_t* new_len = static_cast<int32_t*>(ws);
   int32_t* new_table = new_len + (R + 63) / 64 * 64;
   cache_fork_take<<<R, 256, 0, s>>>(R, P, n_pages, max_pages, from, len, table, ref, new_table, new_len);
