@@ -9,6 +9,9 @@ input generator in workloads.py) does not need the library or a GPU.
 _BINDING_NAMES = (
     "dspark_markov_sample", "dspark_confidence", "dspark_schedule", "dspark_verify",
     "dspark_workspace_size", "dspark_status_string", "load_library", "DSparkError",
+    "dspark_cache_append", "dspark_cache_attention", "dspark_cache_read", "dspark_cache_reset",
+    "dspark_cache_reserve", "dspark_cache_commit", "dspark_cache_fork", "dspark_cache_compact", "dspark_cache_copy",
+    "dspark_cache_page_bytes", "dspark_cache_workspace_size",
 )
 
 
