@@ -183,12 +183,11 @@ struct KTile<DSPARK_CACHE_BF16, D> {
     for (int u = 0; u < D / 16; ++u) x[u] = *reinterpret_cast<const u32x4*>(p + u * 512 + lane);
   }
   static __device__ __forceinline__ int q_dim(int u, int h) { return 16 * u + 8 * h; }
-  template <typename Q>
-  __device__ __forceinline__ f32x16 scores(const Q& q, int) const {
+  __device__ __forceinline__ f32x16 scores(const u32x4 (&q)[D / 16], int) const {
     f32x16 s = {0.f};
 #pragma unroll
     for (int u = 0; u < D / 16; ++u)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(x[u]), as_bf16(q(u)), s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(x[u]), as_bf16(q[u]), s, 0, 0, 0);
     return s;
   }
 };
@@ -217,15 +216,14 @@ struct KTile<DSPARK_CACHE_FP4, D> {
     }
   }
   static __device__ __forceinline__ int q_dim(int u, int h) { return 32 * (2 * (u / 4) + h) + 8 * (u % 4); }
-  template <typename Q>
-  __device__ __forceinline__ f32x16 scores(const Q& q, int h) const {
+  __device__ __forceinline__ f32x16 scores(const u32x4 (&q)[D / 16], int h) const {
     f32x16 s = {0.f};
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
       const float scale = k_scale_value((sc[g / 2] >> (16 * (g & 1) + 8 * h)) & 0xFFu);
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(fp4_octet(x[g][v], scale)), as_bf16(q(4 * g + v)), s, 0, 0,
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(fp4_octet(x[g][v], scale)), as_bf16(q[4 * g + v]), s, 0, 0,
                                                     0);
     }
     return s;
@@ -408,13 +406,11 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   typedef PageLayout<FMT, D> L;
   constexpr int T = W * 64, NB = D / 32, KS = D / 16;
   constexpr float kSlack = 8.f;  // a weight may reach 2^8 before the sums are rescaled
-  // 4-bit heads of 256 dims: output and tiles leave no registers for the query rows
-  constexpr bool kQueryInLds = D == 256 && FMT == DSPARK_CACHE_FP4;
   constexpr bool kShared = FMT == DSPARK_CACHE_BF16;
-  // (the wave's own, under its output, which it writes when done with them)
+  // the waves' outputs, on their way to be joined; before that the ring of 16-bit tiles
   __shared__ f32x4 lds_own[W][NB * 4][64];
   __shared__ float2 lds_ml[W][64];
-  static_assert(NB * 4 >= KS && (NB * 4) % W == 0, "the queries fit under the output; waves share its pieces");
+  static_assert((NB * 4) % W == 0, "waves share an output's pieces");
   __shared__ int64_t lds_scan[W];
   __shared__ int64_t lds_base, lds_run[2];
   __shared__ int2 lds_heads[W];
@@ -615,20 +611,14 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
     const uint32_t k_lane = KTile<FMT, D>::lane_offset(TWO ? col & 15 : col, h);
     const uint32_t v_lane = VTile<FMT, D>::lane_offset(col, h);
 
-    // the query rows' operands: in registers, or the wave's own slice of LDS
-    u32x4 q_reg[kQueryInLds ? 1 : KS];
+    // the query rows' operands
+    u32x4 q[KS];
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
-      u32x4 v = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
+      q[x] = *reinterpret_cast<const u32x4*>(a.q + out_at * D + KTile<FMT, D>::q_dim(x, h));
 #pragma unroll
-      for (int y = 0; y < 4; ++y) v[y] = (v[y] & a.q_keep) ^ a.q_flip;
-      if constexpr (kQueryInLds) lds_own[wave][x][lane] = __builtin_bit_cast(f32x4, v);
-      else q_reg[x] = v;
+      for (int y = 0; y < 4; ++y) q[x][y] = (q[x][y] & a.q_keep) ^ a.q_flip;
     }
-    auto q = [&](int x) {
-      if constexpr (kQueryInLds) return __builtin_bit_cast(u32x4, lds_own[wave][x][lane]);
-      else return q_reg[x];
-    };
 
     // One tile: its scores s, its values, first token ct and pages c0, c1;
     // ahead(): what may run beside the exponentials.
@@ -794,8 +784,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       // Every wave for itself, straight into registers, a tile ahead.  4-bit
       // tiles leave room for the next one's scores, whose products then run
       // beside this one's exponentials (128 requests x up to 17 rows over
-      // ragged contexts up to 16384: 452 -> 419 us with it).
-      constexpr bool kAhead = FMT == DSPARK_CACHE_FP4 && !kQueryInLds;
+      // ragged contexts up to 16384: 452 -> 419 us with it; 64 x up to 17 rows,
+      // heads of 256 dims, up to 4096: 209 -> 197).
+      constexpr bool kAhead = FMT == DSPARK_CACHE_FP4;
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
       KTile<FMT, D> kt;
