@@ -861,60 +861,76 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       }
     }
 
-    // Join the waves along the tokens and write: every wave leaves its output
-    // in LDS and takes an equal share of its rows' dims from all of them.
+    // Write, or leave a part.  Waves along the tokens are joined first: every
+    // wave leaves its output in LDS and takes an equal share of its rows' dims
+    // from all of them.  A wave that has its rows for itself writes from its
+    // registers (32 x 17 rows x 4 query heads a head, over 4096 tokens 108 us
+    // through LDS, 102 so; of 4 bits over 8192 122 and 115).
     const bool opens = t0 == 0, closes = t1 == b.count;
     const bool valid = wq * kTile + col < b.rows;
     const int64_t slot = (static_cast<int64_t>(place_of) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
-    if (active) lds_ml[wave][lane] = make_float2(acc.m, acc.l);
-    __syncthreads();
     const bool whole = opens && closes;
     float m = acc.m, l = 0.f;
-    if (active) {
-      float2 ml[W];
+    // piece x: dims 32 (x / 4) + 8 (x % 4) + 4 h .. of the lane's row
+    auto write = [&](int x, const f32x4& o) {
+      if (!whole) {
+        if (valid) reinterpret_cast<f32x4*>(a.part)[(slot * (NB * 4) + x) * 64 + lane] = o;
+      } else if (valid) {
+        const u32x2 w{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+        *reinterpret_cast<u32x2*>(a.out + out_at * D + (x / 4) * 32 + 8 * (x % 4) + 4 * h) = w;
+      }
+    };
+    auto piece = [&](int x, float f) {
+      const f32x16& y = acc.o[x / 4];
+      const int j = 4 * (x % 4);
+      return f32x4{y[j] * f, y[j + 1] * f, y[j + 2] * f, y[j + 3] * f};
+    };
+    if (WT == 1) {
+      if (active) {
+        l = acc.l + xor32(acc.l);
+        const float f = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-      for (int k = 0; k < W; ++k) ml[k] = k < WT ? lds_ml[wq + k * qt][lane] : make_float2(neg_inf(), 0.f);
+        for (int x = 0; x < NB * 4; ++x) write(x, piece(x, f));
+      }
+    } else {
+      if (active) lds_ml[wave][lane] = make_float2(acc.m, acc.l);
+      __syncthreads();
+      if (active) {
+        float2 ml[W];
 #pragma unroll
-      for (int k = 0; k < W; ++k) m = fmaxf(m, ml[k].x);
-      const float ref = m == neg_inf() ? 0.f : m;
+        for (int k = 0; k < W; ++k) ml[k] = k < WT ? lds_ml[wq + k * qt][lane] : make_float2(neg_inf(), 0.f);
 #pragma unroll
-      for (int k = 0; k < W; ++k) l += ml[k].y * __builtin_amdgcn_exp2f(ml[k].x - ref);
-      l += xor32(l);
-      const float f = __builtin_amdgcn_exp2f(acc.m - ref) * (!whole ? 1.f : l != 0.f ? 1.f / l : 0.f);
+        for (int k = 0; k < W; ++k) m = fmaxf(m, ml[k].x);
+        const float ref = m == neg_inf() ? 0.f : m;
 #pragma unroll
-      for (int x = 0; x < NB; ++x)
+        for (int k = 0; k < W; ++k) l += ml[k].y * __builtin_amdgcn_exp2f(ml[k].x - ref);
+        l += xor32(l);
+        const float f = __builtin_amdgcn_exp2f(acc.m - ref) * (!whole ? 1.f : l != 0.f ? 1.f / l : 0.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          lds_own[wave][x * 4 + j][lane] = f32x4{acc.o[x][4 * j] * f, acc.o[x][4 * j + 1] * f,
-                                                 acc.o[x][4 * j + 2] * f, acc.o[x][4 * j + 3] * f};
-    }
-    __syncthreads();
-    if (active) {
-      // piece x: dims 32 (x / 4) + 8 (x % 4) + 4 h .. of the lane's row
-      const int share = NB * 4 >> (__ffs(WT) - 1);
+        for (int x = 0; x < NB * 4; ++x) lds_own[wave][x][lane] = piece(x, f);
+      }
+      __syncthreads();
+      if (active) {
+        const int share = NB * 4 >> (__ffs(WT) - 1);
 #pragma unroll 2
-      for (int x = wt * share; x < (wt + 1) * share; ++x) {
-        f32x4 o{0.f, 0.f, 0.f, 0.f};
+        for (int x = wt * share; x < (wt + 1) * share; ++x) {
+          f32x4 o{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-          if (k < WT) {
-            const f32x4 y = lds_own[wq + k * qt][x][lane];
+          for (int k = 0; k < W; ++k)
+            if (k < WT) {
+              const f32x4 y = lds_own[wq + k * qt][x][lane];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) o[z] += y[z];
-          }
-        if (!whole) {
-          if (valid) reinterpret_cast<f32x4*>(a.part)[(slot * (NB * 4) + x) * 64 + lane] = o;
-        } else if (valid) {
-          const u32x2 w{bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
-          *reinterpret_cast<u32x2*>(a.out + out_at * D + (x / 4) * 32 + 8 * (x % 4) + 4 * h) = w;
+              for (int z = 0; z < 4; ++z) o[z] += y[z];
+            }
+          write(x, o);
         }
       }
-      if (wt == 0 && h == 0) {
-        if (!whole) a.ml[slot * kTile + col] = make_float2(m, l);
-        else if (a.lse && valid) a.lse[out_at] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
-      }
+      __syncthreads();  // before the next segment's waves write there
     }
-    __syncthreads();  // before the next segment's waves write there
+    if (active && wt == 0 && h == 0) {
+      if (!whole) a.ml[slot * kTile + col] = make_float2(m, l);
+      else if (a.lse && valid) a.lse[out_at] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
+    }
     if (opens) {  // the work group that holds the last tile's first unit has the last part
       const int n = closes ? 0
                     : parts > 0 ? Parts<kFavoured>(b.count, weight, parts, paired).used()
