@@ -13,10 +13,10 @@
 //
 // Latency bounds it: a chain of loads (the length, the page's id, the row),
 // the sines, one pass over the rows.  GPU time with heads of 128 dims and 8
-// heads of keys: one token, 32 query heads, 3.9 us (the sines and what comes
-// before them 2.9); 128 requests of up to 17 packed rows, 56 query heads,
-// 15.6 us, of which V of groups that are not whole, in 2-byte stores, is 1.8;
-// 32 requests x 17 rows into 4-bit pages 12.6 us; 4 x 512 rows 15.6 us.
+// heads of keys: one token, 32 query heads, 3.5 us; 128 requests of up to 17
+// packed rows, 56 query heads, 12.3 us (15.1 with the sums over a head and the
+// rotation's partners through LDS instead of lane patterns), of which V of
+// groups that are not whole, in 2-byte stores, is 1.8; 4 x 512 rows 14.5 us.
 #include "cache.hpp"
 
 namespace dspark {
@@ -48,8 +48,33 @@ __device__ __forceinline__ int small_quotient(int x, float inv) {
   return static_cast<int>((static_cast<float>(x) + 0.5f) * inv);
 }
 
-__device__ __forceinline__ double shfl_xor_t(double x, int o) { return __shfl_xor(x, o); }
-__device__ __forceinline__ float shfl_xor_t(float x, int o) { return __shfl_xor(x, o); }
+// The value of another lane of the same 16 by a fixed pattern, without the
+// way through LDS that a shuffle takes.
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140, kTurn8 = 0x128;
+template <int PATTERN>
+__device__ __forceinline__ int lane_pattern(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, PATTERN, 0xF, 0xF, false);
+}
+template <int PATTERN>
+__device__ __forceinline__ float lane_pattern(float x) {
+  return __int_as_float(lane_pattern<PATTERN>(__float_as_int(x)));
+}
+template <int PATTERN>
+__device__ __forceinline__ double lane_pattern(double x) {
+  return __hiloint2double(lane_pattern<PATTERN>(__double2hiint(x)), lane_pattern<PATTERN>(__double2loint(x)));
+}
+
+// f over the values of L = 4, 8, 16 or 32 neighbouring lanes, the same in each
+// (f commutes, so also the same bits).
+template <int L, typename T, typename F>
+__device__ __forceinline__ T over_lanes(T x, F f) {
+  x = f(x, lane_pattern<kSwap1>(x));
+  x = f(x, lane_pattern<kSwap2>(x));
+  if constexpr (L > 4) x = f(x, lane_pattern<kMirror8>(x));
+  if constexpr (L > 8) x = f(x, lane_pattern<kMirror16>(x));
+  if constexpr (L > 16) x = f(x, __shfl_xor(x, 16));
+  return x;
+}
 
 __device__ __forceinline__ float inv_sqrt(float x) { return rsqrtf(x); }
 __device__ __forceinline__ double inv_sqrt(double x) { return 1.0 / sqrt(x); }
@@ -65,8 +90,7 @@ __device__ __forceinline__ void norm_rotate(T (&x)[8], int li, bool norm, const 
     T ss = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) ss += shfl_xor_t(ss, o);
+    ss = over_lanes<L>(ss, [](T p, T q) { return p + q; });
     const T s = inv_sqrt(ss * static_cast<T>(1.0 / D) + static_cast<T>(eps));
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -89,6 +113,17 @@ __device__ __forceinline__ void norm_rotate(T (&x)[8], int li, bool norm, const 
   const int lane = threadIdx.x & 63, base = lane - li;
   const bool first = li < hl, second = !first && li < 2 * hl;
   const int partner = base + (first ? li + hl : second ? li - hl : li);
+  if constexpr (L == 16)
+    if (2 * hl == L) {  // all of a head of 128 dims: the partner is 8 lanes away in the same 16
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const T y = lane_pattern<kTurn8>(x[e]);
+        const int i = (li & 7) * 8 + e;
+        const T c = cs[2 * i], s = cs[2 * i + 1];
+        x[e] = first ? x[e] * c - y * s : x[e] * c + y * s;
+      }
+      return;
+    }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const T y = __shfl(x[e], partner);
@@ -136,11 +171,8 @@ __device__ __forceinline__ void store_k_fp4(const double (&x)[8], int li, char* 
     top = fmax(top, fabs(x[e]));
     bad |= !(fabs(x[e]) < 3.4028236692093846e38);  // 2^128
   }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    top = fmax(top, shfl_xor_t(top, o));
-    bad |= __shfl_xor(static_cast<int>(bad), o) != 0;
-  }
+  top = over_lanes<4>(top, [](double p, double q) { return fmax(p, q); });
+  bad = over_lanes<4>(static_cast<int>(bad), [](int p, int q) { return p | q; }) != 0;
   int e2 = -126;
   if (top > 0 && !bad) {
     e2 = ilogb(top) - 2;                    // top / 2^e2 in [4, 8)
@@ -206,11 +238,8 @@ __device__ __forceinline__ void store_v_fp4(const uint16_t* src, int li, int j, 
     top = fmaxf(top, fabsf(f[e]));
     bad |= !(fabsf(f[e]) <= 3.4028234e38f);
   }
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) {
-    top = fmaxf(top, __shfl_xor(top, o));
-    bad |= __shfl_xor(static_cast<int>(bad), o) != 0;
-  }
+  top = over_lanes<kLanes>(top, [](float p, float q) { return fmaxf(p, q); });
+  bad = over_lanes<kLanes>(static_cast<int>(bad), [](int p, int q) { return p | q; }) != 0;
   // 6 |v| against the borders times max |v|: products of 16-bit values with
   // numbers of at most 3 bits, exact in fp32; above 2^100 both sides are
   // scaled down first so that they stay finite
@@ -464,8 +493,8 @@ hipError_t append_run(AppendArgs& a, hipStream_t s) {
   const int64_t gx = static_cast<int64_t>(a.R) * a.groups;
   // a round of head slots a work group where there are few token groups, else
   // about 12 work groups a compute unit (4 at a time): 128 x 17 packed rows and
-  // 4 x 512 rows take 16.1 and 16.0 us, with 6 a unit 17.2 and 15.6, with 24
-  // 16.6 and 18.6; 32 x 17 rows of 4-bit pages 16.7, 18.7 and 16.6 with their read
+  // 4 x 512 rows take 12.3 and 14.5 us, with 8 a unit 11.9 and 15.0, with 24
+  // 14.0 and 17.8; 32 x 17 rows of 4-bit pages with their read 15.8, 16.9, 15.9
   const int v_units = FMT == DSPARK_CACHE_FP4 ? kGroup * a.Hkv + kGroup - 1 : kGroup * a.Hkv;
   const int most = ceil_div(kGroup * (a.Hq + a.Hkv) + v_units, kHeads);
   const int64_t want = 12LL * compute_units() / gx;
