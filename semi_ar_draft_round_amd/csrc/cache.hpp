@@ -90,4 +90,41 @@ __device__ __forceinline__ u32x4 fp4_octet(uint32_t w, float scale) {
   return u32x4{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale), fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)};
 }
 
+// The value of another lane by a fixed pattern, without the way through LDS
+// that a shuffle takes; 0 in rows of 16 lanes outside ROWS and where the
+// pattern has no source.  All lanes involved are active.
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140, kTurn8 = 0x128;
+constexpr int kUp1 = 0x111, kUp2 = 0x112, kUp4 = 0x114, kUp8 = 0x118, kLast16 = 0x142, kLast32 = 0x143;
+template <int PATTERN, int ROWS = 0xF>
+__device__ __forceinline__ int lane_pattern(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, PATTERN, ROWS, 0xF, false);
+}
+template <int PATTERN, int ROWS = 0xF>
+__device__ __forceinline__ float lane_pattern(float x) {
+  return __int_as_float(lane_pattern<PATTERN, ROWS>(__float_as_int(x)));
+}
+template <int PATTERN, int ROWS = 0xF>
+__device__ __forceinline__ double lane_pattern(double x) {
+  return __hiloint2double(lane_pattern<PATTERN, ROWS>(__double2hiint(x)),
+                          lane_pattern<PATTERN, ROWS>(__double2loint(x)));
+}
+template <int PATTERN, int ROWS = 0xF>
+__device__ __forceinline__ int64_t lane_pattern(int64_t x) {
+  const uint32_t lo = lane_pattern<PATTERN, ROWS>(static_cast<int>(x));
+  return static_cast<int64_t>(lane_pattern<PATTERN, ROWS>(static_cast<int>(x >> 32))) << 32 | lo;
+}
+
+// f over the values of this lane and those before it, for f with f(x, 0) = x.
+// All 64 lanes are active.
+template <typename T, typename F>
+__device__ __forceinline__ T wave_scan(T x, F f) {
+  x = f(x, lane_pattern<kUp1>(x));
+  x = f(x, lane_pattern<kUp2>(x));
+  x = f(x, lane_pattern<kUp4>(x));
+  x = f(x, lane_pattern<kUp8>(x));
+  x = f(x, lane_pattern<kLast16, 0xA>(x));  // the sums of 16 into the next 16,
+  x = f(x, lane_pattern<kLast32, 0xC>(x));  // that of the first 32 into the others
+  return x;
+}
+
 }  // namespace dspark

@@ -48,22 +48,6 @@ __device__ __forceinline__ int small_quotient(int x, float inv) {
   return static_cast<int>((static_cast<float>(x) + 0.5f) * inv);
 }
 
-// The value of another lane of the same 16 by a fixed pattern, without the
-// way through LDS that a shuffle takes.
-constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140, kTurn8 = 0x128;
-template <int PATTERN>
-__device__ __forceinline__ int lane_pattern(int x) {
-  return __builtin_amdgcn_update_dpp(0, x, PATTERN, 0xF, 0xF, false);
-}
-template <int PATTERN>
-__device__ __forceinline__ float lane_pattern(float x) {
-  return __int_as_float(lane_pattern<PATTERN>(__float_as_int(x)));
-}
-template <int PATTERN>
-__device__ __forceinline__ double lane_pattern(double x) {
-  return __hiloint2double(lane_pattern<PATTERN>(__double2hiint(x)), lane_pattern<PATTERN>(__double2loint(x)));
-}
-
 // f over the values of L = 4, 8, 16 or 32 neighbouring lanes, the same in each
 // (f commutes, so also the same bits).
 template <int L, typename T, typename F>

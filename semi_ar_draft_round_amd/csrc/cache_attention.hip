@@ -472,15 +472,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       longest = max(longest, count * weight);
     }
     if (pass == 0) {
-      int64_t incl = sum;
-      int heads_incl = heads;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int64_t t = __shfl_up(incl, o);
-        const int n = __shfl_up(heads_incl, o);
-        if (lane >= o) incl += t, heads_incl += n;
-        longest = max(longest, __shfl_xor(longest, o));
-      }
+      const int64_t incl = wave_scan(sum, [](int64_t p, int64_t q) { return p + q; });
+      const int heads_incl = wave_scan(heads, [](int p, int q) { return p + q; });
+      longest = wave_scan(longest, [](int p, int q) { return max(p, q); });
       if (lane == 63) {
         lds_scan[wave] = incl;
         lds_heads[wave] = make_int2(heads_incl, longest);

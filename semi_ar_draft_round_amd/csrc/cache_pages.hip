@@ -17,12 +17,7 @@ constexpr int kT = 1024;  // threads of the single-work-group kernels
 // Exclusive prefix sum of one int per thread over the work group; *total gets the sum.
 __device__ int block_exclusive_scan(int v, int* lds, int* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int t = __shfl_up(x, o);
-    if (lane >= o) x += t;
-  }
+  const int x = wave_scan(v, [](int p, int q) { return p + q; });
   if (lane == 63) lds[wave] = x;
   __syncthreads();
   int before = 0, sum = 0;
