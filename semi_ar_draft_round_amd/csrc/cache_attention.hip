@@ -281,8 +281,8 @@ struct VTile<DSPARK_CACHE_FP4, D> {
   }
 };
 
-// Running softmax of a lane's query row (m is the row's, l the lane's own
-// tokens') and its part of the output.
+// Running softmax of a lane's query row (m, what weights are relative to, is
+// the row's, l the lane's own tokens') and its part of the output.
 template <int D>
 struct Acc {
   float m, l;
@@ -405,7 +405,10 @@ template <int FMT, int D, bool TWO>
 __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tiles(AttnArgs a) {
   typedef PageLayout<FMT, D> L;
   constexpr int T = W * 64, NB = D / 32, KS = D / 16;
-  constexpr float kSlack = 8.f;  // a weight may reach 2^8 before the sums are rescaled
+  // The weights' reference is put 8 (in base 2) beyond the maximum, and moves
+  // again once a score passes it: weights are at most 1, so that sums stay as
+  // far from overflow as those of a plain softmax, and few tiles rescale.
+  constexpr float kSlack = 8.f;
   constexpr bool kShared = FMT == DSPARK_CACHE_BF16;
   // the waves' outputs, on their way to be joined; before that the ring of 16-bit tiles
   __shared__ f32x4 lds_own[W][NB * 4][64];
@@ -631,9 +634,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 #pragma unroll
       for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
       top = fmaxf(top, xor32(top)) * a.scale_log2;
-      // weights are relative to acc.m, which follows the maximum once that is 2^8 ahead
-      if (__any(top > acc.m + kSlack)) {
-        const float m = fmaxf(acc.m, top);
+      if (__any(top > acc.m)) {
+        const float m = top > acc.m ? top + kSlack : acc.m;
         const float keep = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(acc.m - m);
         acc.l *= keep;
         acc.m = m;

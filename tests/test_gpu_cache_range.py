@@ -1,0 +1,100 @@
+"""The paged cache's operators at the ends of the values' range: what a plain
+softmax or norm in the same types gives has to come out, without infinities of
+its own."""
+
+import sys
+
+import numpy as np
+import pytest
+
+from cache_cases import BF16, FP4, attention_tolerance, bf, page_bytes
+from oracle import cache as OC
+from semi_ar_draft_round_amd.workloads import bf16_to_f32
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from semi_ar_draft_round_amd import binding
+    binding.load_library()
+    return torch.device("cuda:0")
+
+
+def t16(bits, dev):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).to(dev)
+
+
+def back(t):
+    return bf16_to_f32(t.cpu().view(torch.int16).numpy().view(np.uint16)).astype(np.float64)
+
+
+def one_request(fmt, k, v, P):
+    """A pool of one request's tokens and its table.  k, v: what write_pages takes."""
+    codes = k if fmt == BF16 else k[0]
+    T, H, D = codes.shape
+    n = -(-T // P)
+    pool = np.full((n + 1, page_bytes(fmt, H, D, P)), 0xFF, dtype=np.uint8)
+    table = np.random.default_rng(0).permutation(n + 1)[:n].astype(np.int32)
+    OC.write_pages(fmt, k, v, table, P, pool)
+    return pool, table[None]
+
+
+def attend(dev, fmt, pool, table, q, first, P, heads_kv):
+    """q [rows][Hq][D] bits at positions first ..; float64 out and lse."""
+    from semi_ar_draft_round_amd import binding as B
+    rows = q.shape[0]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)
+    lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=dev)
+    out, _ = B.dspark_cache_attention(t16(q, dev), torch.from_numpy(pool).to(dev), torch.from_numpy(table).to(dev),
+                                      i32(first), i32(rows - 1), rows - 1, fmt=fmt, page=P, heads_kv=heads_kv, lse=lse)
+    return back(out), lse.cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP4])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("power", [115, -90])
+def test_values_far_from_one(power, D, fmt, dev):
+    """Values near 2^power.  16 tokens x 8 query heads fill four row tiles, so
+    a wave goes through tiles in turn; the first has scores of 0, the others
+    of 5.3, and in every fourth row of -5.3 (2^7.65 and 2^-7.65): less than
+    8 ln 2 above the first.  |v| adds up to less than 300 * 6 * 2^115 < 2^126,
+    which the header allows; weights relative to the first tile's maximum
+    would reach 2^7.6 and 32 of them times 2^116 overflow.  At 2^-90 weights
+    are above 2^-24, so that their product with a scale is a normal number.
+
+    The bound is attention_tolerance's for the values divided by 2^power, a
+    power of two, so every relative rounding is the same."""
+    say(f"[range] attention fmt {fmt} D {D} 2^{power}")
+    rng = np.random.default_rng(D + fmt)
+    T, rows, Hq, P = 300, 16, 8, 32
+    late = np.arange(T) >= 32
+    if fmt == BF16:
+        kb, k = bf(np.where(late, 0.5, 0.0)[:, None, None] * np.ones((T, 1, D)))
+        vb, v = bf(rng.uniform(1, 4, (T, 1, D)))
+        stored = bf(v * 2.0 ** power)[0]
+        pool, table = one_request(fmt, kb, stored, P)
+    else:
+        kc = np.where(late, 2, 0)[:, None, None].astype(np.uint8) * np.ones((1, 1, D), np.uint8)
+        kb = np.full((T, 1, D // 32), 126, np.uint8)
+        vc = rng.integers(2, 8, (T, 1, D)).astype(np.uint8)
+        vs = rng.uniform(0.25, 1, (T, 1)).astype(np.float32)
+        k, v = OC.E2M1[kc] * 0.5, OC.E2M1[vc] * vs.astype(np.float64)[..., None]
+        pool, table = one_request(fmt, (kc, kb), (vc, vs * np.float32(2.0 ** power)), P)
+    a = {64: 1.328125, 128: 0.9375, 256: 0.6640625}[D]
+    qb, q = bf(np.where(np.arange(rows) % 4 == 3, -a, a)[:, None, None] * np.ones((rows, Hq, D)))
+    pos = T - rows + np.arange(rows)
+    o, lse = attend(dev, fmt, pool, table, qb, T - rows, P, 1)
+    want, wz = OC.attention(q, k, v, pos, D ** -0.5, 0, 0)
+    tol, tz = attention_tolerance(q, k, v, pos, D ** -0.5, 0, 0, want)
+    assert np.isfinite(o).all()
+    err = np.abs(o / 2.0 ** power - want)
+    assert np.all(err <= tol), float((err / tol).max())
+    assert np.all(np.abs(lse - wz) <= tz + 2.0 ** -22 * np.abs(wz))
