@@ -192,8 +192,9 @@ def acceptance(d: DeviceRound):
     B.dspark_acceptance(d.target, d.U, d.W1, d.W2t, d.x0, d.x, d.lse, c_star=d.c_star, ws=d.ws_accept)
 
 
-def verify(d: DeviceRound):
-    B.dspark_verify(d.target, d.U, d.W1, d.W2t, d.x0, d.x, d.lse, d.logit, d.ell, d.u_acc,
+def verify(d: DeviceRound, ell: Optional[torch.Tensor] = None):
+    """Verification of the admitted drafts: d.ell[r] of them, or ell[r]."""
+    B.dspark_verify(d.target, d.U, d.W1, d.W2t, d.x0, d.x, d.lse, d.logit, d.ell if ell is None else ell, d.u_acc,
                     d.u_res, n_acc=d.n_acc, next_tok=d.next_tok, ws=d.ws_verify)
 
 
@@ -219,13 +220,17 @@ def run_round_cached(d: DeviceRound, cache, forward):
     pages for the admitted rows after the schedule, forward(d, cache, ell) as
     the target's pass over them (cache.append and cache.attend per layer; its
     logits go to d.target), and after the verification the accepted rows
-    kept.  A request that got no pages (ell -1) keeps its cache as it was;
-    its n_acc and next_tok are then of no use."""
+    kept.  A request that got no pages (ell -1) keeps its cache as it was and
+    has to draft from the same anchor again: its next_tok is its x0, and its
+    n_acc is -1."""
     sample_conf(d)
     schedule(d)
     ell = cache.reserve(d.ell, d.gamma)
     forward(d, cache, ell)
-    verify(d)
+    verify(d, ell)
+    refused = ell < 0
+    torch.where(refused, d.x0, d.next_tok, out=d.next_tok)
+    d.n_acc.masked_fill_(refused, -1)
     cache.commit(d.n_acc)
 
 
