@@ -202,7 +202,7 @@ dspark_status dspark_cache_reset(int R, int n_pages, int max_pages, int32_t* tab
  *   ell_out [R] i32 out; pairs [R][2] i32 out (the first n_pairs);
  *   n_pairs [1] i32 out; status [1] i32 out or NULL: DSPARK_OK, or
  *   DSPARK_ENOPAGES if a request was refused
- *   ws      DSPARK_CACHE_WS_RESERVE bytes
+ *   ws      DSPARK_CACHE_WS_RESERVE bytes, 16-byte aligned
  * ell_out may be ell.
  */
 dspark_status dspark_cache_reserve(int R, int gamma, int P, int n_pages, int max_pages, const int32_t* ell,
@@ -229,7 +229,7 @@ dspark_status dspark_cache_commit(int R, int gamma, int P, int n_pages, int max_
  * map is allowed (a permutation, one source for many, chains): all sources
  * are read as they were.
  *
- *   from [R] i32; ws DSPARK_CACHE_WS_FORK bytes
+ *   from [R] i32; ws DSPARK_CACHE_WS_FORK bytes, 16-byte aligned
  */
 dspark_status dspark_cache_fork(int R, int P, int n_pages, int max_pages, const int32_t* from, int32_t* len,
                                 int32_t* table, int32_t* ref, uint32_t* bits, void* ws, size_t ws_bytes,
@@ -242,7 +242,7 @@ dspark_status dspark_cache_fork(int R, int P, int n_pages, int max_pages, const 
  * dspark_cache_copy what to move before the cache is used again.
  *
  *   pairs [n_pages / 2][2] i32 out (the first n_pairs), n_pairs [1] i32 out
- *   ws    DSPARK_CACHE_WS_COMPACT bytes
+ *   ws    DSPARK_CACHE_WS_COMPACT bytes, 16-byte aligned
  */
 dspark_status dspark_cache_compact(int R, int n_pages, int max_pages, int32_t* table, int32_t* ref, uint32_t* bits,
                                    int32_t* pairs, int32_t* n_pairs, void* ws, size_t ws_bytes, void* stream);

@@ -590,8 +590,8 @@ def _cache_ws(ws, kind, R, gamma, a, b, c, dev):
     if ws is None:
         return torch.empty(max(1, dspark_cache_workspace_size(kind, R, gamma, a, b, c)), dtype=_U8,
                            device=torch.device("cuda", dev))
-    if ws.dtype is not _U8 or not ws.is_contiguous() or ws.get_device() != dev:
-        raise ValueError("ws must be a contiguous uint8 tensor on the call's device")
+    if ws.dtype is not _U8 or not ws.is_contiguous() or ws.get_device() != dev or ws.data_ptr() % 16 != 0:
+        raise ValueError("ws must be a contiguous, 16-byte aligned uint8 tensor on the call's device")
     return ws
 
 

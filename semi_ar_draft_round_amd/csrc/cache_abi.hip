@@ -166,7 +166,9 @@ dspark_status dspark_cache_reserve(int R, int gamma, int P, int n_pages, int max
                                    int32_t* ell_out, int32_t* pairs, int32_t* n_pairs, int32_t* status, void* ws,
                                    size_t ws_bytes, void* stream) {
   if (!batch_ok(R, gamma) || !page_ok(P) || !pages_ok(R, n_pages, max_pages)) return DSPARK_EINVAL;
-  if (!ell || !len || !table || !ref || !bits || !ell_out || !pairs || !n_pairs) return DSPARK_EINVAL;
+  if (!ell || !len || !table || !ref || !bits || !ell_out || !pairs || !n_pairs ||
+      !aligned(static_cast<const char*>(ws)))
+    return DSPARK_EINVAL;
   if (!ws || ws_bytes < dspark_cache_workspace_size(DSPARK_CACHE_WS_RESERVE, R, gamma, max_pages, n_pages, 0))
     return DSPARK_EWORKSPACE;
   dspark_status st = check_device();
@@ -191,7 +193,7 @@ dspark_status dspark_cache_fork(int R, int P, int n_pages, int max_pages, const 
                                 int32_t* table, int32_t* ref, uint32_t* bits, void* ws, size_t ws_bytes,
                                 void* stream) {
   if (!page_ok(P) || !pages_ok(R, n_pages, max_pages)) return DSPARK_EINVAL;
-  if (!from || !len || !table || !ref || !bits) return DSPARK_EINVAL;
+  if (!from || !len || !table || !ref || !bits || !aligned(static_cast<const char*>(ws))) return DSPARK_EINVAL;
   if (!ws || ws_bytes < dspark_cache_workspace_size(DSPARK_CACHE_WS_FORK, R, 0, max_pages, n_pages, 0))
     return DSPARK_EWORKSPACE;
   dspark_status st = check_device();
@@ -203,7 +205,7 @@ dspark_status dspark_cache_fork(int R, int P, int n_pages, int max_pages, const 
 dspark_status dspark_cache_compact(int R, int n_pages, int max_pages, int32_t* table, int32_t* ref, uint32_t* bits,
                                    int32_t* pairs, int32_t* n_pairs, void* ws, size_t ws_bytes, void* stream) {
   if (!pages_ok(R, n_pages, max_pages)) return DSPARK_EINVAL;
-  if (!table || !ref || !bits || !pairs || !n_pairs) return DSPARK_EINVAL;
+  if (!table || !ref || !bits || !pairs || !n_pairs || !aligned(static_cast<const char*>(ws))) return DSPARK_EINVAL;
   if (!ws || ws_bytes < dspark_cache_workspace_size(DSPARK_CACHE_WS_COMPACT, R, 0, max_pages, n_pages, 0))
     return DSPARK_EWORKSPACE;
   dspark_status st = check_device();

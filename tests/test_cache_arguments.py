@@ -1,0 +1,52 @@
+"""Refusals of the paged cache's calls and of its binding, without a GPU
+(nothing here reaches the device): what the header asks of workspaces and
+numbers."""
+
+import ctypes
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "semi_ar_draft_round_amd", "libdspark.so")
+
+EINVAL, EWORKSPACE = 1, 3
+P = ctypes.c_void_p
+FAKE = P(0x1000)   # never dereferenced
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(LIB):
+        from semi_ar_draft_round_amd import build
+        build.build()
+    from semi_ar_draft_round_amd import binding
+    return binding.load_library(LIB)
+
+
+@pytest.mark.parametrize("at", [0x1001, 0x1004, 0x1008])
+def test_workspaces_are_16_byte_aligned(at, lib):
+    ws = P(at)
+    p = FAKE
+    assert lib.dspark_cache_reserve(4, 3, 16, 64, 8, p, p, p, p, p, p, p, p, None, ws, BIG, None) == EINVAL
+    assert lib.dspark_cache_fork(4, 16, 64, 8, p, p, p, p, p, ws, BIG, None) == EINVAL
+    assert lib.dspark_cache_compact(4, 64, 8, p, p, p, p, p, ws, BIG, None) == EINVAL
+    assert lib.dspark_cache_attention(1, 4, 3, 8, 2, 128, 64, 50, 4, p, 0.1, 0, 0, None, p, p, p, p, p, None, ws, BIG,
+                                      None) == EINVAL
+    for call in (lambda w: lib.dspark_cache_reserve(4, 3, 16, 64, 8, p, p, p, p, p, p, p, p, None, w, BIG, None),
+                 lambda w: lib.dspark_cache_fork(4, 16, 64, 8, p, p, p, p, p, w, BIG, None),
+                 lambda w: lib.dspark_cache_compact(4, 64, 8, p, p, p, p, p, w, BIG, None)):
+        assert call(None) == EWORKSPACE
+
+
+def test_the_binding_checks_a_given_workspace(lib):
+    import torch
+    from semi_ar_draft_round_amd import binding as B
+    ws = torch.zeros(4096 + 64, dtype=torch.uint8)
+    lead = -ws.data_ptr() % 16
+    kind = B.CACHE_WS_RESERVE
+    assert B._cache_ws(ws[lead:], kind, 4, 0, 8, 64, 0, -1) is not None
+    for off in (1, 4, 8):
+        with pytest.raises(ValueError, match="aligned"):
+            B._cache_ws(ws[lead + off:], kind, 4, 0, 8, 64, 0, -1)
