@@ -1017,7 +1017,8 @@ __global__ __launch_bounds__(256) void cache_attention_join(AttnArgs a) {
   if (a.lse && x0 == 0 && lane < 32) a.lse[out_at] = l != 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : neg_inf();
 }
 
-constexpr int kMaxGrid = 1024;
+// Work groups at most: two on each of a gfx950's 256 compute units.
+constexpr int kMaxGrid = 512;
 
 int slot_tiles_of(int gamma, int Hq, int Hkv) {
   const int64_t rows = static_cast<int64_t>(gamma + 1) * (Hq / Hkv);

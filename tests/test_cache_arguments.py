@@ -50,3 +50,16 @@ def test_the_binding_checks_a_given_workspace(lib):
     for off in (1, 4, 8):
         with pytest.raises(ValueError, match="aligned"):
             B._cache_ws(ws[lead + off:], kind, 4, 0, 8, 64, 0, -1)
+
+
+def test_the_attention_workspace_holds_what_a_device_uses(lib):
+    """Two parts for each of at most 512 work groups (256 with 256 dims): 32
+    rows a row tile of D fp32 sums, a maximum and a sum; and the descriptors,
+    32 bytes a work group.  No more than that, rounded to 256 bytes."""
+    from semi_ar_draft_round_amd import binding as B
+    for D in (64, 128, 256):
+        for gamma, heads, tiles in ((0, 4, 1), (16, 4, 3), (1023, 1, 4), (1023, 8, 4)):
+            groups = 256 if D == 256 else 512
+            need = 512 * 32 + groups * 2 * tiles * 32 * (4 * D + 8)
+            got = B.dspark_cache_workspace_size(B.CACHE_WS_ATTENTION, 7, gamma, 8 * heads, 8, D)
+            assert need <= got < need + 256, (D, gamma, heads)
