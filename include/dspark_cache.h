@@ -100,7 +100,8 @@ size_t dspark_cache_workspace_size(dspark_cache_ws_kind kind, int R, int gamma, 
  * adjacent != 0 a = 2 i, b = 2 i + 1; dims rot .. D - 1 are not rotated.
  * q heads use wq and go to q_out, k heads wk; v is stored as it is.  Angles
  * are fp64 (reduced to a turn before the fp32 sine and cosine), the rest
- * fp32, rounded once; keys of 4-bit pages are fp64 throughout.
+ * fp32 (the norm of a head in fp64 where its squares leave fp32's range),
+ * rounded once; keys of 4-bit pages are fp64 throughout.
  *
  *   q      bf16, row i at q + i * ldq: [Hq][D]; ldq >= Hq * D; likewise k, v
  *          with [Hkv][D] (views of one fused projection are fine); ldq, ldk

@@ -7,7 +7,7 @@ import sys
 import numpy as np
 import pytest
 
-from cache_cases import BF16, FP4, attention_tolerance, bf, page_bytes
+from cache_cases import BF16, F32, FP4, HALF, attention_tolerance, bf, page_bytes
 from oracle import cache as OC
 from semi_ar_draft_round_amd.workloads import bf16_to_f32
 
@@ -98,3 +98,36 @@ def test_values_far_from_one(power, D, fmt, dev):
     err = np.abs(o / 2.0 ** power - want)
     assert np.all(err <= tol), float((err / tol).max())
     assert np.all(np.abs(lse - wz) <= tz + 2.0 ** -22 * np.abs(wz))
+
+
+@pytest.mark.parametrize("fmt", [BF16, FP4])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norms_of_large_and_small_heads(eps, D, fmt, dev):
+    """Rows of every magnitude that bf16 has, side by side: the square of
+    2^100 is past fp32's range and that of 2^-100 below it, the norm is not.
+    The bound is the append's: 32 roundings of fp32 doubled, then half a step
+    of bf16.  A 4-bit key is off by at most one unit 2^e, top > 3.5 * 2^e."""
+    from semi_ar_draft_round_amd import binding as B
+    say(f"[range] norms fmt {fmt} D {D} eps {eps}")
+    rng = np.random.default_rng(D)
+    power = np.array([0, 59, 60, 61, 62, 63, 64, 100, 127, -1, -47, -48, -49, -62, -64, -74, -100, -120, 0, 127])
+    rows, Hq, Hkv, P = len(power), 3, 2, 32
+    x = rng.uniform(0.25, 1, (rows, Hq + 2 * Hkv, D)) * rng.choice([-1, 1], (rows, Hq + 2 * Hkv, D))
+    xb, x = bf(x * 2.0 ** power[:, None, None])
+    wb, w = bf(1 + 0.3 * rng.standard_normal((2, D)))
+    xt = t16(xb, dev)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+    pool = torch.full((2, B.dspark_cache_page_bytes(fmt, Hkv, D, P)), 255, dtype=torch.uint8, device=dev)
+    table = i32(1, 0).view(1, 2)
+    q = B.dspark_cache_append(xt[:, :Hq], xt[:, Hq:Hq + Hkv], xt[:, Hq + Hkv:], pool, table, i32(0), i32(rows - 1),
+                              rows - 1, fmt=fmt, page=P, wq=t16(wb[0], dev), wk=t16(wb[1], dev), eps=eps)
+    k, _ = B.dspark_cache_read(pool, table, None, i32(rows), rows, fmt=fmt, page=P, heads_kv=Hkv, dim=D)
+    z = OC.norm(x[:, :Hq], w[0], eps)
+    assert np.all(np.abs(back(q) - z) <= (HALF + 64 * F32) * np.abs(z) + 2.0 ** -134)
+    z, kd = OC.norm(x[:, Hq:Hq + Hkv], w[1], eps), back(k)[0]
+    if fmt == BF16:
+        assert np.all(np.abs(kd - z) <= (HALF + 64 * F32) * np.abs(z) + 2.0 ** -134)
+    else:
+        top = np.abs(z).reshape(rows, Hkv, -1, 32).max(-1).repeat(32, -1)
+        assert np.all(np.abs(kd - z) <= np.maximum(top * (2 / 7) * (1 + 2.0 ** -20), 2.0 ** -126))
