@@ -342,16 +342,15 @@ __global__ __launch_bounds__(kThreads, 4) void cache_append_kernel(AppendArgs a)
     const double f = i == static_cast<int>(threadIdx.x) || kThreads % half == 0 ? freq0 : a.freq[p];
     const double turns = static_cast<double>(t0 + row) * f * 0.15915494309189535;
     const double t = turns - rint(turns);
+    // queries always get the fp32 ones, whatever else this run holds: a row's
+    // bits do not depend on how the work is cut
     float s, c;
+    sincospif(2.f * static_cast<float>(t), &s, &c);
     if (FMT == DSPARK_CACHE_FP4 && row >= k_a && row <= k_b) {
       double s64, c64;
       sincospi(2.0 * t, &s64, &c64);
       cs64[FMT == DSPARK_CACHE_FP4 ? row * D + 2 * p : 0] = c64;
       cs64[FMT == DSPARK_CACHE_FP4 ? row * D + 2 * p + 1 : 0] = s64;
-      s = static_cast<float>(s64);
-      c = static_cast<float>(c64);
-    } else {
-      sincospif(2.f * static_cast<float>(t), &s, &c);
     }
     cs[row * D + 2 * p] = c;
     cs[row * D + 2 * p + 1] = s;
