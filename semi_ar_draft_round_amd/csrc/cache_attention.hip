@@ -383,9 +383,15 @@ __device__ __forceinline__ int waves_along(int fmt, int D, int shift) {
 // Moves a wave's 64 x 16 bytes from memory to LDS at byte `to`, lane by lane,
 // past the registers.  Counts as an outstanding vector load; the compiler
 // does not know of it, so its waits may be longer than they need to be, never
-// shorter, and the reader's wait is written out below.
+// shorter, and the reader's wait is written out below.  M0, which holds the
+// address and which the compiler reserves for itself, is left as it was.
 __device__ __forceinline__ void copy_to_lds(const char* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(to), "v"(from)
+      : "memory");
 }
 
 // Outstanding vector loads down to N, LDS reads down to none, then the work

@@ -63,3 +63,21 @@ def test_the_attention_workspace_holds_what_a_device_uses(lib):
             need = 512 * 32 + groups * 2 * tiles * 32 * (4 * D + 8)
             got = B.dspark_cache_workspace_size(B.CACHE_WS_ATTENTION, 7, gamma, 8 * heads, 8, D)
             assert need <= got < need + 256, (D, gamma, heads)
+
+
+def test_inline_assembly_leaves_m0_as_it_was():
+    """The compiler keeps M0 for itself and is not told of writes to it, so an
+    asm statement that writes it saves it first and puts it back."""
+    import glob
+    import re
+    seen = 0
+    for path in glob.glob(os.path.join(ROOT, "semi_ar_draft_round_amd", "csrc", "*.h*")):
+        for text in re.findall(r"\basm volatile\((.*?)\);", open(path).read(), flags=re.S):
+            lines = [x.strip() for x in "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', text.split("\n      :")[0])).replace(
+                "\\t", "").split("\\n")]
+            if not any(re.match(r"\w+ m0\b", x) for x in lines):
+                continue
+            seen += 1
+            save = re.match(r"s_mov_b32 (%\d), m0$", lines[0])
+            assert save and lines[-1] == f"s_mov_b32 m0, {save.group(1)}", path
+    assert seen == 1
