@@ -84,7 +84,7 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale) {
 
 // Eight codes times the scale of a K scale byte b: 2^(b - 127), or NaN for
 // 255.  The conversion reads the scale's exponent field as such a byte: 255
-// gives NaN for every code, 0 gives 2^-127 (both checked on the device).
+// gives NaN for every code, 0 gives 2^-127.
 __device__ __forceinline__ float k_scale_value(uint32_t b) { return __uint_as_float(b << 23); }
 __device__ __forceinline__ u32x4 fp4_octet(uint32_t w, float scale) {
   return u32x4{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale), fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)};

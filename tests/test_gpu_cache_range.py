@@ -131,3 +131,74 @@ def test_norms_of_large_and_small_heads(eps, D, fmt, dev):
     else:
         top = np.abs(z).reshape(rows, Hkv, -1, 32).max(-1).repeat(32, -1)
         assert np.all(np.abs(kd - z) <= np.maximum(top * (2 / 7) * (1 + 2.0 ** -20), 2.0 ** -126))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_every_key_scale_reads_back(D, dev):
+    """Tokens whose K scale bytes go through 0 (2^-127), 1 .. 252 and 255
+    (NaN): the values that the header names, exactly."""
+    from semi_ar_draft_round_amd import binding as B
+    say(f"[range] scales read D {D}")
+    rng = np.random.default_rng(D)
+    scale = np.concatenate([np.arange(253), [255, 0, 255]])
+    T, E, P = len(scale), D // 32, 64
+    kc = rng.integers(0, 16, (T, 1, D)).astype(np.uint8)
+    kb = np.stack([np.roll(scale, i) for i in range(E)], -1)[:, None].astype(np.uint8)
+    pool, table = one_request(FP4, (kc, kb), (kc, np.ones((T, 1), np.float32)), P)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+    k, _ = B.dspark_cache_read(torch.from_numpy(pool).to(dev), torch.from_numpy(table).to(dev), None, i32(T), T, fmt=FP4,
+                               page=P, heads_kv=1, dim=D)
+    s = np.repeat(np.where(kb == 255, np.nan, 2.0 ** (kb.astype(np.float64) - 127)), 32, axis=-1)
+    assert np.array_equal(back(k)[0], np.where(kc & 8, -1.0, 1.0) * OC.E2M1[kc & 7] * s, equal_nan=True)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt,byte", [(FP4, 0), (FP4, 1), (FP4, 20), (FP4, 234), (FP4, 252), (BF16, 0), (BF16, 252)])
+def test_keys_far_from_one(fmt, byte, D, dev):
+    """Visible keys whose scale is 2^(byte - 127), the smallest ones subnormal
+    in bf16, against queries that bring the scores back to the order of one."""
+    say(f"[range] keys fmt {fmt} byte {byte} D {D}")
+    rng = np.random.default_rng(D + byte)
+    T, rows, Hq, P = 70, 6, 4, 32
+    kc = rng.integers(0, 16, (T, 1, D)).astype(np.uint8)
+    k = np.where(kc & 8, -1.0, 1.0) * OC.E2M1[kc & 7] * 2.0 ** (byte - 127)
+    if fmt == FP4:
+        vc, vs = rng.integers(0, 16, (T, 1, D)).astype(np.uint8), rng.uniform(0.1, 0.6, (T, 1)).astype(np.float32)
+        v = np.where(vc & 8, -1.0, 1.0) * OC.E2M1[vc & 7] * vs.astype(np.float64)[..., None]
+        pool, table = one_request(FP4, (kc, np.full((T, 1, D // 32), byte, np.uint8)), (vc, vs), P)
+    else:
+        vb, v = bf(rng.standard_normal((T, 1, D)))
+        kb, same = bf(k)
+        assert np.array_equal(same, k)
+        pool, table = one_request(BF16, kb, vb, P)
+    qb, q = bf(rng.uniform(0.25, 1, (rows, Hq, D)) * rng.choice([-1, 1], (rows, Hq, D)) * 2.0 ** min(126, 126 - byte))
+    pos = T - rows + np.arange(rows)
+    o, lse = attend(dev, fmt, pool, table, qb, T - rows, P, 1)
+    want, wz = OC.attention(q, k, v, pos, D ** -0.5, 0, 0)
+    tol, tz = attention_tolerance(q, k, v, pos, D ** -0.5, 0, 0, want)
+    err = np.abs(o - want)
+    assert np.all(err <= tol), float((err / tol).max())
+    assert np.all(np.abs(lse - wz) <= tz + 2.0 ** -22 * np.abs(wz))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_visible_nan_scales(D, dev):
+    """A NaN scale of a visible key makes the rows that see it NaN, of a
+    visible value too, and leaves the other rows alone."""
+    say(f"[range] NaN scales D {D}")
+    rng = np.random.default_rng(D)
+    T, rows, P = 70, 6, 32
+    for what in ("key", "value"):
+        kc, vc = (rng.integers(0, 16, (T, 2, D)).astype(np.uint8) for _ in range(2))
+        kb, vs = rng.integers(123, 127, (T, 2, D // 32)).astype(np.uint8), rng.uniform(0.1, 0.6, (T, 2)).astype(np.float32)
+        if what == "key":
+            kb[T - 3, 1, D // 32 - 1] = 255
+        else:
+            vs[T - 3, 1] = np.nan
+        pool, table = one_request(FP4, (kc, kb), (vc, vs), P)
+        qb, q = bf(rng.standard_normal((rows, 4, D)))
+        o, lse = attend(dev, FP4, pool, table, qb, T - rows, P, 2)
+        sees = np.zeros((rows, 4), dtype=bool)
+        sees[3:, 2:] = True                            # positions T - 3 .. of the heads that read head 1
+        assert np.array_equal(np.isnan(o).all(-1), sees) and np.array_equal(np.isnan(o).any(-1), sees)
+        assert np.array_equal(np.isnan(lse), sees if what == "key" else np.zeros_like(sees))
