@@ -149,7 +149,7 @@ dspark_status dspark_cache_append(int fmt, int R, int gamma, int Hq, int Hkv, in
  *   ws   dspark_cache_workspace_size(DSPARK_CACHE_WS_ATTENTION, R, gamma, Hq,
  *        Hkv, D) bytes, 16-byte aligned; contents on entry are irrelevant
  *
- * Limits: as append; Hq a multiple of Hkv; scale finite.
+ * Limits: as append; Hq a multiple of Hkv; |scale| <= 2^126.
  */
 dspark_status dspark_cache_attention(int fmt, int R, int gamma, int Hq, int Hkv, int D, int P, int n_pages,
                                      int max_pages, const void* q, float scale, int window, int sinks,

@@ -125,7 +125,7 @@ dspark_status dspark_cache_attention(int fmt, int R, int gamma, int Hq, int Hkv,
   if (!batch_ok(R, gamma) || !heads_ok(Hq) || !heads_ok(Hkv) || Hq % Hkv != 0 || !dim_ok(D) || !page_ok(P) ||
       !pages_ok(R, n_pages, max_pages))
     return DSPARK_EINVAL;
-  if (window < 0 || sinks < 0 || !isfinite(scale)) return DSPARK_EINVAL;
+  if (window < 0 || sinks < 0 || !(fabsf(scale) <= 0x1p126f)) return DSPARK_EINVAL;  // times log2 e: still finite
   if (!q || !ell || !len || !table || !pool || !out) return DSPARK_EINVAL;
   if (!aligned(static_cast<const char*>(q), static_cast<const char*>(pool), static_cast<const char*>(out),
                static_cast<const char*>(ws)))

@@ -81,3 +81,14 @@ def test_inline_assembly_leaves_m0_as_it_was():
             save = re.match(r"s_mov_b32 (%\d), m0$", lines[0])
             assert save and lines[-1] == f"s_mov_b32 m0, {save.group(1)}", path
     assert seen == 1
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.0 ** 126 * 1.001, float("inf"), float("nan")])
+def test_scales_that_overflow_in_base_two(scale, lib):
+    """The kernel works with scale * log2 e, which has to be finite; the
+    workspace is checked after it, so an accepted scale gets as far as that."""
+    p = FAKE
+    call = lambda s: lib.dspark_cache_attention(1, 4, 3, 8, 2, 128, 64, 50, 4, p, s, 0, 0, None, p, p, p, p, p, None, p, 16,
+                                                None)
+    assert call(scale) == EINVAL
+    assert call(2.0 ** 126) == EWORKSPACE and call(-2.0 ** 126) == EWORKSPACE and call(0.0) == EWORKSPACE
