@@ -555,13 +555,23 @@ def dspark_sts_fit(z, n_acc, grid, n_bins=15, ws=None):
 
 # ---------------------------------------------------------------- the paged cache
 
+def _int32(*numbers):
+    """ctypes cuts an int to 32 bits without a word: 2^32 tokens of a window
+    would be none."""
+    for x in numbers:
+        if not -0x80000000 <= x <= 0x7FFFFFFF:
+            raise ValueError(f"{x} does not fit 32 bits")
+
+
 @functools.lru_cache(maxsize=None)   # a function of small integers
 def dspark_cache_page_bytes(fmt: int, heads_kv: int, dim: int, page: int) -> int:
+    _int32(fmt, heads_kv, dim, page)
     return int(load_library().dspark_cache_page_bytes(fmt, heads_kv, dim, page))
 
 
 @functools.lru_cache(maxsize=4096)
 def dspark_cache_workspace_size(kind: int, R: int, gamma: int, a: int, b: int, c: int = 0) -> int:
+    _int32(kind, R, gamma, a, b, c)
     return int(load_library().dspark_cache_workspace_size(kind, R, gamma, a, b, c))
 
 
@@ -615,6 +625,7 @@ def _check_rows(t, name, rows, heads, dim, dev):
 def _batch(table, length, ell, gamma, row0, rows, dev):
     """R, max_pages and the addresses of row0, ell, length and table."""
     R, max_pages = table.shape
+    _int32(gamma)
     if row0 is None and rows != R * (gamma + 1):
         raise ValueError(f"{rows} rows: without row0 there are R * (gamma + 1) = {R * (gamma + 1)}")
     return (R, max_pages, None if row0 is None else _need(row0, "row0", (R,), _I32, dev),
@@ -685,6 +696,7 @@ def dspark_cache_attention(q, pool, table, length, ell, gamma, *, fmt, page, hea
         out = torch.empty((rows, Hq, D), dtype=_BF, device=q.device)
     p_out = _need(out, "out", (rows, Hq, D), _BF, dev)
     p_lse = None if lse is None else _need(lse, "lse", (rows, Hq), torch.float32, dev)
+    _int32(window, sinks)
     stream = _raw_stream(dev)
     if rows == 0:
         return out, lse
@@ -741,6 +753,7 @@ def dspark_cache_reserve(table, length, ref, bits, ell, gamma, *, page, ell_out=
     (-1 where a request was refused), pairs [R][2], n_pairs [1] (page copies
     for dspark_cache_copy) and status [1] (0 or ENOPAGES), all int32."""
     R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    _int32(gamma, page)
     new = lambda *shape: torch.empty(shape, dtype=_I32, device=table.device)
     p_ell = _need(ell, "ell", (R,), _I32, dev)
     ell_out = new(R) if ell_out is None else ell_out
@@ -761,6 +774,7 @@ def dspark_cache_commit(table, length, ref, bits, ell, n_acc, gamma, *, page, wi
     """Keep rows 0 .. n_acc[r] of every request with ell[r] >= 0; release the
     pages past them and, with a window, those no later row can see."""
     R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    _int32(gamma, page, window, sinks)
     st = load_library().dspark_cache_commit(R, gamma, page, n_pages, max_pages, window, sinks,
                                             _need(ell, "ell", (R,), _I32, dev), _need(n_acc, "n_acc", (R,), _I32, dev),
                                             p_len, p_table, p_ref, p_bits, _raw_stream(dev))
@@ -771,6 +785,7 @@ def dspark_cache_fork(table, length, ref, bits, parent, *, page, ws=None):
     """Request r takes over what parent[r] held before the call (r: stays as
     it is; -1: empty)."""
     R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    _int32(page)
     p_parent = _need(parent, "parent", (R,), _I32, dev)
     stream = _raw_stream(dev)
     ws = _cache_ws(ws, CACHE_WS_FORK, R, 0, max_pages, n_pages, 0, dev)

@@ -34,8 +34,8 @@ class PagedCache:
         if nb == 0 or layers < 1 or slots < 1 or max_tokens < 1 or n_pages < 1:
             raise ValueError(f"no cache of {layers} layers, {slots} slots, {max_tokens} tokens, {n_pages} pages of "
                              f"{page} tokens, {heads_kv} heads of {dim}, format {fmt}")
-        if window < 0 or sinks < 0:
-            raise ValueError("window and sinks must not be negative")
+        if not 0 <= window <= 0x7FFFFFFF or not 0 <= sinks <= 0x7FFFFFFF:
+            raise ValueError("window and sinks must be 0 .. 2^31 - 1")
         self.heads_kv, self.dim, self.page, self.fmt = heads_kv, dim, page, fmt
         self.window, self.sinks = window, sinks
         i32 = dict(dtype=torch.int32, device=dev)

@@ -92,3 +92,38 @@ def test_scales_that_overflow_in_base_two(scale, lib):
                                                 None)
     assert call(scale) == EINVAL
     assert call(2.0 ** 126) == EWORKSPACE and call(-2.0 ** 126) == EWORKSPACE and call(0.0) == EWORKSPACE
+
+
+def test_numbers_past_32_bits_are_refused(lib):
+    """Cut to 32 bits, a window of 2^32 tokens would be none at all, 2^32 + 4
+    first tokens would be 4."""
+    import torch
+    from semi_ar_draft_round_amd import binding as B
+    from semi_ar_draft_round_amd.cache import PagedCache
+    i32, wide = dict(dtype=torch.int32), 1 << 32
+    table, ell, length = torch.zeros(2, 3, **i32), torch.zeros(2, **i32), torch.zeros(2, **i32)
+    ref, bits = torch.zeros(9, **i32), torch.zeros(1, **i32)
+    pool = torch.zeros(9, B.dspark_cache_page_bytes(1, 2, 64, 16), dtype=torch.uint8)
+    q, k = torch.zeros(4, 4, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    state = (table, length, ref, bits)
+    for call in (lambda x: B.dspark_cache_page_bytes(1, 2, 64, x + 16),
+                 lambda x: B.dspark_cache_workspace_size(B.CACHE_WS_ATTENTION, 4, x + 3, 8, 2, 64),
+                 lambda x: B.dspark_cache_append(q, k, k, pool, table, length, ell, x + 1, fmt=1, page=16, row0=ell),
+                 lambda x: B.dspark_cache_append(q, k, k, pool, table, length, ell, 1, fmt=1, page=x + 16),
+                 lambda x: B.dspark_cache_attention(q, pool, table, length, ell, 1, fmt=1, page=16, heads_kv=2, window=x),
+                 lambda x: B.dspark_cache_attention(q, pool, table, length, ell, 1, fmt=1, page=16, heads_kv=2, window=5,
+                                                    sinks=x + 4),
+                 lambda x: B.dspark_cache_read(pool, table, None, ell, 1, fmt=1, page=x + 16, heads_kv=2, dim=64),
+                 lambda x: B.dspark_cache_reserve(*state, ell, x + 1, page=16),
+                 lambda x: B.dspark_cache_reserve(*state, ell, 1, page=x + 16),
+                 lambda x: B.dspark_cache_commit(*state, ell, ell, 1, page=16, window=x),
+                 lambda x: B.dspark_cache_commit(*state, ell, ell, 1, page=16, window=8, sinks=x + 4),
+                 lambda x: B.dspark_cache_commit(*state, ell, ell, x + 1, page=16),
+                 lambda x: B.dspark_cache_fork(*state, ell, page=x + 16)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call(wide)
+        with pytest.raises(ValueError, match="32 bits"):
+            call(-wide)
+    for bad in (dict(window=wide), dict(sinks=wide + 4)):
+        with pytest.raises(ValueError, match="window and sinks"):
+            PagedCache(1, 2, 10, 4, 1, 64, device="cpu", **bad)
