@@ -137,11 +137,13 @@ dspark_status dspark_cache_append(int fmt, int R, int gamma, int Hq, int Hkv, in
  * key/value head h / (Hq / Hkv).  What an invisible token holds, infinities
  * and NaN too, has no effect.  Scores, maxima and sums are fp32; the weights
  * exp(s_j - m), m at most 8 ln 2 above the running maximum and never below it,
- * are rounded to bf16 for the product with v (a relative 2^-8 each at most, the
- * same as the output's own rounding), 4-bit V with its token's scale multiplied
- * into the weight first.  Weights are at most 1: out is finite where the scores
- * are and the visible tokens' |v| of a dim (4 bits: of a head's largest) add up
- * to less than 2^127.
+ * are carried as two bf16 numbers each (2^-16 of a weight is lost) into the
+ * product with v, 4-bit V with its token's scale multiplied into the weight
+ * first; the output is rounded once.  Weights are at most 1: out is finite
+ * where the scores are and the visible tokens' |v| of a dim (4 bits: of a
+ * head's largest) add up to less than 2^127.  How the tokens are cut into
+ * parts follows from the whole batch, so a row's last bits do too; the same
+ * call gives the same bits.
  *
  *   q    [rows][Hq][D] bf16 (q_out of append); out [rows][Hq][D] bf16 out
  *   lse  [rows][Hq] f32 out, or NULL

@@ -230,6 +230,34 @@ struct KTile<DSPARK_CACHE_FP4, D> {
   }
 };
 
+// Weights as two bf16 numbers each, the nearest and the nearest to what that
+// leaves: 2^-16 of a weight is lost.
+struct Weights {
+  u32x4 near, rest;
+  __device__ __forceinline__ void set(int j, float w0, float w1) {
+    near[j] = bf16_pair(w0, w1);
+    rest[j] = bf16_pair(w0 - __uint_as_float(near[j] << 16), w1 - __uint_as_float(near[j] & 0xFFFF0000u));
+  }
+};
+
+// o += V^T W^T for two blocks of 32 dims, in turn so that no product waits
+// for the one before it.
+//
+// One bf16 number a weight put as much error into the output as the output's
+// own rounding: 2.3e-3 of it in all against float64 (up to 2.8e-3 where few
+// tokens matter), 1.66e-3 so, as with fp32 weights.  What the second costs:
+// 128 requests x up to 17 rows of 16 bits 547 -> 558 us, one request over
+// 131055 tokens 119 -> 121, window 51.7 -> 56.8, 4 x 512 rows 111 -> 122; of 4
+// bits 423 -> 495, single tokens 89 -> 97.  fp16 weights in a unit that follows
+// the row's largest took 446 of 4 bits, but lose tokens below 2^-24 of it,
+// and with them the dims that nothing larger reaches.
+__device__ __forceinline__ void add_weighted(f32x16& o0, f32x16& o1, u32x4 v0, u32x4 v1, const Weights& w) {
+  o0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v0), as_bf16(w.near), o0, 0, 0, 0);
+  o1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v1), as_bf16(w.near), o1, 0, 0, 0);
+  o0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v0), as_bf16(w.rest), o0, 0, 0, 0);
+  o1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v1), as_bf16(w.rest), o1, 0, 0, 0);
+}
+
 template <int D>
 struct VTile<DSPARK_CACHE_BF16, D> {
   u32x4 x[2][D / 32];
@@ -714,9 +742,6 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         sum += p[j];
       }
       acc.l += sum;
-      u32x4 pk[2];
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) pk[j / 8][(j % 8) / 2] = bf16_pair(vt.weight(j, p[j]), vt.weight(j + 1, p[j + 1]));
       bool odd = false;
       if constexpr (FMT == DSPARK_CACHE_BF16) {
         if (!clear) {
@@ -744,11 +769,14 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         }
       }
 #pragma unroll
-      for (int s2 = 0; s2 < 2; ++s2)
+      for (int s2 = 0; s2 < 2; ++s2) {
+        Weights w;
 #pragma unroll
-        for (int x = 0; x < NB; ++x)
-          acc.o[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vt.operand(s2, x)), as_bf16(pk[s2]), acc.o[x], 0,
-                                                             0, 0);
+        for (int j = 0; j < 8; j += 2) w.set(j / 2, vt.weight(8 * s2 + j, p[8 * s2 + j]), vt.weight(8 * s2 + j + 1, p[8 * s2 + j + 1]));
+#pragma unroll
+        for (int x = 0; x < NB; x += 2)
+          add_weighted(acc.o[x], acc.o[x + 1], vt.operand(s2, x), vt.operand(s2, x + 1), w);
+      }
       if constexpr (FMT == DSPARK_CACHE_BF16)
         if (__any(odd)) {
           uint32_t visible = 0;
