@@ -27,11 +27,15 @@
 //
 // What bounds it, with 8 heads of 128 dims: the pages' bytes for 16 bits (128
 // requests of up to 17 rows x 7 query heads a head, ragged contexts up to
-// 8192: 536 us, 4.9 TB/s; one request x 17 rows over 131072 tokens 118 us, 4.6
-// TB/s) and for single tokens of 4 bits (32 requests over 16384 tokens 89 us,
-// 4.0 TB/s); the vector units for many rows of 4 bits (the same 128 requests
-// up to 16384 tokens 419 us, two fifths of it the exponentials and their
-// sums); and for short contexts the two launches and the chain of loads before
+// 8192: 556 us, 4.7 TB/s; one request x 17 rows over 131072 tokens 123 us, 4.4
+// TB/s) and mostly for single tokens of 4 bits (32 requests over 16384 tokens
+// 97 us, 3.7 TB/s).  Many rows of 4 bits (the same 128 requests up to 16384
+// tokens 505 us) are bound by the order inside a wave: vector instructions
+// take 47 % of the issue slots and products 33 % of the matrix units' time,
+// and with two waves a SIMD neither hides the other whole.  Heads of 256 dims
+// have one wave a SIMD, where nothing but the wave itself does; 65 .. 96 query
+// rows are three row tiles, and the fourth wave of the work group idles.
+// Short contexts are bound by the two launches and the chain of loads before
 // the first tile, 6 of 13 us (one token over 1023).
 #include "cache.hpp"
 
@@ -106,7 +110,8 @@ constexpr int kFar = 1 << 29;  // past every table (2^20 pages of 128 tokens)
 
 // Units of a tile by the log2 of the waves along the rows: the time it takes.
 // 16-bit tiles come at the pace of memory until four waves share them; 4-bit
-// ones at that of the vector units nearly from the start.
+// ones at that of the vector units nearly from the start.  Measured with heads
+// of 128 dims, as kRestart and kFavour below.
 __device__ __forceinline__ int weight_of(int fmt, int shift) {
   return fmt == DSPARK_CACHE_BF16 ? 2 + shift : (shift == 0 ? 2 : shift == 1 ? 4 : 7);
 }
@@ -246,11 +251,13 @@ struct Weights {
 // One bf16 number a weight put as much error into the output as the output's
 // own rounding: 2.3e-3 of it in all against float64 (up to 2.8e-3 where few
 // tokens matter), 1.66e-3 so, as with fp32 weights.  What the second costs:
-// 128 requests x up to 17 rows of 16 bits 547 -> 558 us, one request over
-// 131055 tokens 119 -> 121, window 51.7 -> 56.8, 4 x 512 rows 111 -> 122; of 4
-// bits 423 -> 495, single tokens 89 -> 97.  fp16 weights in a unit that follows
-// the row's largest took 446 of 4 bits, but lose tokens below 2^-24 of it,
-// and with them the dims that nothing larger reaches.
+// 128 requests x up to 17 rows of 16 bits 547 -> 556 us, one request over
+// 131055 tokens 119 -> 123, window 51.7 -> 56.8, 4 x 512 rows 111 -> 122, 16 x
+// 17 rows with heads of 256 dims 192 -> 230; of 4 bits the 128 requests 424 ->
+// 505, single tokens 89 -> 97.  fp16 weights in a unit that follows the row's
+// largest took 446 for 4 bits, but lose tokens below 2^-24 of it, and with them
+// the dims that nothing larger reaches; to choose by tile would let a row's
+// bits depend on the rows beside it.
 __device__ __forceinline__ void add_weighted(f32x16& o0, f32x16& o1, u32x4 v0, u32x4 v1, const Weights& w) {
   o0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v0), as_bf16(w.near), o0, 0, 0, 0);
   o1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v1), as_bf16(w.near), o1, 0, 0, 0);
@@ -356,12 +363,11 @@ constexpr int kRestart = 16;
 
 // Of two work groups on a compute unit the one that came first is served
 // first.  Where the vector units set the pace (4-bit heads of 64 and 128 dims)
-// it is through with an equal share after 421 us when the other takes 499
-// (128 requests x 17 rows over 8192 tokens), so it gets more, in 64ths of an
-// equal share: 454 -> 446 us over ragged contexts up to 16384, 132 -> 125 us
-// for 32 requests over 8192 (4 and 10 of 64: 457 and 454, 125 and 124).  At
-// the pace of memory it makes no difference (16-bit pages: 545 and 539 us,
-// 254 and 254 us), and short runs lose: only from 4 kMinUnits a work group on.
+// it is through with an equal share after 85 % of the other's time, so it gets
+// more, in 64ths of an equal share: 545 -> 511 us for 128 requests x up to 17
+// rows over ragged contexts up to 16384, 142 -> 135 us for 32 x 17 rows over
+// 8192.  At the pace of memory it makes no difference (16-bit pages: within 1
+// %), and short runs lose: only from 4 kMinUnits a work group on.
 constexpr int kFavour = 7;
 
 // A head in `parts` parts of `tiles` tiles, the last ones perhaps empty; with
@@ -869,8 +875,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       // Every wave for itself, straight into registers, a tile ahead.  4-bit
       // tiles leave room for the next one's scores, whose products then run
       // beside this one's exponentials (128 requests x up to 17 rows over
-      // ragged contexts up to 16384: 452 -> 419 us with it; 64 x up to 17 rows,
-      // heads of 256 dims, up to 4096: 209 -> 197).
+      // ragged contexts up to 16384: 550 -> 511 us with it; 64 x 17 rows, heads
+      // of 256 dims, up to 4096: 363 -> 322).
       constexpr bool kAhead = FMT == DSPARK_CACHE_FP4;
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
@@ -949,8 +955,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
     // Write, or leave a part.  Waves along the tokens are joined first: every
     // wave leaves its output in LDS and takes an equal share of its rows' dims
     // from all of them.  A wave that has its rows for itself writes from its
-    // registers (32 x 17 rows x 4 query heads a head, over 4096 tokens 108 us
-    // through LDS, 102 so; of 4 bits over 8192 122 and 115).
+    // registers (32 x 17 rows x 4 query heads a head, over 4096 tokens 112 us
+    // through LDS, 106 so; of 4 bits over 8192 140 and 135).
     const bool opens = t0 == 0, closes = t1 == b.count;
     const bool valid = wq * kTile + col < b.rows;
     const int64_t slot = (static_cast<int64_t>(place_of) * 2 + (opens ? 1 : 0)) * a.slot_tiles + wq;
