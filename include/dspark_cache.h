@@ -137,7 +137,7 @@ dspark_status dspark_cache_append(int fmt, int R, int gamma, int Hq, int Hkv, in
  * key/value head h / (Hq / Hkv).  What an invisible token holds, infinities
  * and NaN too, has no effect.  Scores, maxima and sums are fp32; the weights
  * exp(s_j - m), m at most 8 ln 2 above the running maximum and never below it,
- * are carried as two bf16 numbers each (2^-16 of a weight is lost) into the
+ * are carried as two bf16 numbers each (2^-15 of a weight is lost) into the
  * product with v, 4-bit V with its token's scale multiplied into the weight
  * first; the output is rounded once.  Weights are at most 1: out is finite
  * where the scores are and the visible tokens' |v| of a dim (4 bits: of a

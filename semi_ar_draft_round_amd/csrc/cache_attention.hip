@@ -235,13 +235,19 @@ struct KTile<DSPARK_CACHE_FP4, D> {
   }
 };
 
-// Weights as two bf16 numbers each, the nearest and the nearest to what that
-// leaves: 2^-16 of a weight is lost.
+// Weights as two bf16 numbers each: the upper half of the bits, which is not
+// above the weight, and the nearest to what that leaves and 2^-22 of the weight
+// on top.  2^-15 of a weight is lost; both are positive where the weight is, so
+// that an infinite value times them is infinite, and neither zero nor of the
+// other sign.
 struct Weights {
-  u32x4 near, rest;
+  u32x4 upper, rest;
   __device__ __forceinline__ void set(int j, float w0, float w1) {
-    near[j] = bf16_pair(w0, w1);
-    rest[j] = bf16_pair(w0 - __uint_as_float(near[j] << 16), w1 - __uint_as_float(near[j] & 0xFFFF0000u));
+    constexpr float kMore = 1.f + 0x1p-22f;
+    const uint32_t b0 = __float_as_uint(w0), b1 = __float_as_uint(w1);
+    upper[j] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+    rest[j] = bf16_pair(__builtin_fmaf(w0, kMore, -__uint_as_float(b0 & 0xFFFF0000u)),
+                        __builtin_fmaf(w1, kMore, -__uint_as_float(b1 & 0xFFFF0000u)));
   }
 };
 
@@ -253,14 +259,14 @@ struct Weights {
 // tokens matter), 1.66e-3 so, as with fp32 weights.  What the second costs:
 // 128 requests x up to 17 rows of 16 bits 547 -> 556 us, one request over
 // 131055 tokens 119 -> 123, window 51.7 -> 56.8, 4 x 512 rows 111 -> 122, 16 x
-// 17 rows with heads of 256 dims 192 -> 230; of 4 bits the 128 requests 424 ->
-// 505, single tokens 89 -> 97.  fp16 weights in a unit that follows the row's
+// 17 rows with heads of 256 dims 192 -> 224; of 4 bits the 128 requests 424 ->
+// 505, single tokens 89 -> 95.  fp16 weights in a unit that follows the row's
 // largest took 446 for 4 bits, but lose tokens below 2^-24 of it, and with them
 // the dims that nothing larger reaches; to choose by tile would let a row's
 // bits depend on the rows beside it.
 __device__ __forceinline__ void add_weighted(f32x16& o0, f32x16& o1, u32x4 v0, u32x4 v1, const Weights& w) {
-  o0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v0), as_bf16(w.near), o0, 0, 0, 0);
-  o1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v1), as_bf16(w.near), o1, 0, 0, 0);
+  o0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v0), as_bf16(w.upper), o0, 0, 0, 0);
+  o1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v1), as_bf16(w.upper), o1, 0, 0, 0);
   o0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v0), as_bf16(w.rest), o0, 0, 0, 0);
   o1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(v1), as_bf16(w.rest), o1, 0, 0, 0);
 }

@@ -202,3 +202,33 @@ def test_visible_nan_scales(D, dev):
         sees[3:, 2:] = True                            # positions T - 3 .. of the heads that read head 1
         assert np.array_equal(np.isnan(o).all(-1), sees) and np.array_equal(np.isnan(o).any(-1), sees)
         assert np.array_equal(np.isnan(lse), sees if what == "key" else np.zeros_like(sees))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows,Hq", [(1, 1), (5, 8), (16, 8)])
+def test_infinities_that_every_row_sees(rows, Hq, D, dev):
+    """Infinite values of tokens far below every row's position, where no tile
+    needs a mask: they come out as infinities with their sign, two of unlike
+    sign in a dim as NaN, and every other dim as if they were not there."""
+    say(f"[range] infinities D {D} rows {rows}")
+    rng = np.random.default_rng(D + rows)
+    T, P = 700, 32
+    kb, k = bf(rng.standard_normal((T, 1, D)))
+    vb, v = bf(rng.standard_normal((T, 1, D)))
+    v[40, 0, 3] = v[41, 0, 3] = v[300, 0, 3] = np.inf
+    v[41, 0, 7] = -np.inf
+    v[130, 0, D - 1] = -np.inf
+    v[333, 0, 20], v[500, 0, 20] = np.inf, -np.inf
+    vb[~np.isfinite(v)] = np.where(v[~np.isfinite(v)] > 0, 0x7F80, 0xFF80)
+    pool, table = one_request(BF16, kb, vb, P)
+    qb, q = bf(rng.standard_normal((rows, Hq, D)))
+    pos = T - rows + np.arange(rows)
+    o, _ = attend(dev, BF16, pool, table, qb, T - rows, P, 1)
+    with np.errstate(invalid="ignore"):
+        want, _ = OC.attention(q, k, v, pos, D ** -0.5, 0, 0)
+    assert np.array_equal(np.isnan(o), np.isnan(want)) and np.isnan(want[..., 20]).all()
+    assert np.array_equal(np.isposinf(o), np.isposinf(want)) and np.isposinf(want[..., 3]).all()
+    assert np.array_equal(np.isneginf(o), np.isneginf(want)) and np.isneginf(want[..., [7, D - 1]]).all()
+    fine = np.isfinite(want)
+    tol, _ = attention_tolerance(q, k, v, pos, D ** -0.5, 0, 0, np.where(fine, want, 0))
+    assert np.all(np.abs(np.where(fine, o, 0) - np.where(fine, want, 0)) <= np.where(fine, tol, 0))
