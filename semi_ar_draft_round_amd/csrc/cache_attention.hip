@@ -784,7 +784,10 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       for (int s2 = 0; s2 < 2; ++s2) {
         Weights w;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) w.set(j / 2, vt.weight(8 * s2 + j, p[8 * s2 + j]), vt.weight(8 * s2 + j + 1, p[8 * s2 + j + 1]));
+        for (int j = 0; j < 8; j += 2) {
+          const int t = 8 * s2 + j;
+          w.set(j / 2, vt.weight(t, p[t]), vt.weight(t + 1, p[t + 1]));
+        }
 #pragma unroll
         for (int x = 0; x < NB; x += 2)
           add_weighted(acc.o[x], acc.o[x + 1], vt.operand(s2, x), vt.operand(s2, x + 1), w);
