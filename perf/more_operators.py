@@ -35,7 +35,7 @@ import torch
 own = False
 
 EPS = 1e-6
-BF16, FP4, FP8 = 1, 2, 3
+BF16, FP4, FP8 = 1, 2, 4
 LOW, HIGH = -117, 119  # exponents that a block's scale may have
 
 
@@ -680,7 +680,7 @@ def _plain_evict(s):
     rank = torch.empty_like(order).scatter_(1, order, col.expand_as(order))
     gone = may & (rank < over[:, None])
     _count(s["ref"], torch.where(gone, T, -1), -1)
-    T.masked_fill_(gone, -1)
+    T.masked_fill_(gone, -2)  # no page, and evicted
     s["mass"].masked_fill_(gone, 0)
     s["freed"].copy_(gone.sum(1))
     s["bits"].copy_(_free_bits(s["ref"]))
