@@ -13,17 +13,21 @@
  *   dspark_cache_attention  the rows' attention over the pages, optionally
  *                           with a sliding window and visible first tokens
  *   dspark_cache_read       cached tokens as dense rows
+ *   dspark_cache_weigh      the attention weights that the tokens of every
+ *                           page got from the rows, added up
  *   dspark_cache_reset      an empty cache
  *   dspark_cache_reserve    pages for a round's rows (copy on write)
  *   dspark_cache_commit     keep the accepted rows, release the other pages
  *   dspark_cache_fork       requests take over other requests' caches (beams,
  *                           shared prompts), or let go of their own
+ *   dspark_cache_evict      pages of least weight let go, down to a budget
  *   dspark_cache_compact    the pages in use drawn together at the low ids
  *   dspark_cache_copy       the page copies the calls above ask for
  *
  * A round over one layer's pool, in stream order:
  *   dspark_schedule (ell) -> reserve (ell_out) -> copy -> for each layer
- *   append and attention (ell_out) -> dspark_verify (n_acc) -> commit.
+ *   append and attention (ell_out) -> dspark_verify (n_acc) -> commit; with a
+ * budget of pages, weigh after every layer's attention and evict after commit.
  *
  * The conventions of dspark.h hold (device pointers, 16-byte aligned, owned
  * by the caller; nothing allocated, synchronised or read on the host; safe to
@@ -50,6 +54,13 @@
  *                       [i][e]), V scales [P] f32.  Two codes a byte, low
  *                       nibble first; a code is e2m1: a sign bit and the
  *                       magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   DSPARK_CACHE_FP8    [Hkv] of: K codes [P/16][D/16][16 tokens][16 dims], V
+ *                       codes [P/16][2][32][E][8 tokens] (dim e * 32 + i at
+ *                       [i][e]), K scales [8] u8, V scales [8] u8, one for
+ *                       each block of 16 tokens (2^(b - 127); those past P/16
+ *                       unused).  A code is e4m3: a sign, four exponent bits
+ *                       (bias 7), three of the magnitude; 0x7F and 0xFF are
+ *                       NaN, there are no infinities, the largest is 448.
  *
  * 4-bit rounding: codes are the nearest, ties to the even code.  K: a scale
  * 2^e per 32 dims, the smallest that brings them to at most 7 (7 rounds to 6
@@ -57,6 +68,16 @@
  * bf16 inputs, so a code does not depend on the order of a sum.  V: one scale
  * per token and head, max|v| / 6 in fp32; codes by exact comparison.  A group
  * with a NaN, or a value at or past 2^128, has a NaN scale.
+ *
+ * 8-bit rounding: a block's scale for K, and for V, is the smallest 2^e, -117
+ * <= e <= 119, that brings what the block holds to at most 448 (larger values
+ * are held as 448 2^119); codes are the nearest, ties to the even code,
+ * computed in fp64 from the bf16 inputs.  Tokens join a block as they are
+ * appended, and the scale only grows: where it does, the codes of the block's
+ * committed tokens are rounded again, which is exact but for values below
+ * 2^-6 of the scale.  So a token that is appended and rolled back can leave a
+ * larger scale behind, up to the next block.  Infinities and NaN are held as
+ * NaN and have no part in the scale.
  */
 #ifndef DSPARK_CACHE_H
 #define DSPARK_CACHE_H
@@ -70,7 +91,7 @@ extern "C" {
 /* Device status of dspark_cache_reserve: a request got no pages. */
 #define DSPARK_ENOPAGES 7
 
-typedef enum { DSPARK_CACHE_BF16 = 1, DSPARK_CACHE_FP4 = 2 } dspark_cache_format;
+typedef enum { DSPARK_CACHE_BF16 = 1, DSPARK_CACHE_FP4 = 2, DSPARK_CACHE_FP8 = 4 } dspark_cache_format;
 
 /* Workspace selectors for dspark_cache_workspace_size. */
 typedef enum {
@@ -101,7 +122,7 @@ size_t dspark_cache_workspace_size(dspark_cache_ws_kind kind, int R, int gamma, 
  * q heads use wq and go to q_out, k heads wk; v is stored as it is.  Angles
  * are fp64 (reduced to a turn before the fp32 sine and cosine), the rest
  * fp32 (the norm of a head in fp64 where its squares leave fp32's range),
- * rounded once; keys of 4-bit pages are fp64 throughout.
+ * rounded once; keys of 4-bit and 8-bit pages are fp64 throughout.
  *
  *   q      bf16, row i at q + i * ldq: [Hq][D]; ldq >= Hq * D; likewise k, v
  *          with [Hkv][D] (views of one fused projection are fine); ldq, ldk
@@ -168,14 +189,45 @@ dspark_status dspark_cache_attention(int fmt, int R, int gamma, int Hq, int Hkv,
  * zero.  4-bit values are exact in bf16 for K, and rounded once for V.
  *
  *   start NULL: 0.  Limits: as append; 1 <= T <= 2^26.
+ * 8-bit values are exact in bf16.
  */
 dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, int n_pages, int max_pages,
                                 const int32_t* start, const int32_t* count, const int32_t* table, const void* pool,
                                 void* k, void* v, void* stream);
 
 /*
+ * dspark_cache_weigh — how much attention every page gets: for a request with
+ * rows, for each entry s of its table,
+ *   mass[r][s] <- keep * mass[r][s] + sum exp(scale * q . k_j - lse)
+ * over the rows, the query heads and the tokens j of page s that the row sees
+ * (dspark_cache_attention's rule and its lse).  Requests without rows are left
+ * as they were.  Every row and head shares out 1 over
+ * the pages it sees.  Drafts count whether they are accepted or not; called
+ * with n_acc in the place of ell, before commit, only the rows that stay do.
+ * The layers of a model share a table, so a round calls it once per layer with
+ * one mass: keep < 1 (older rounds fade) for the first, 1 for the others.
+ *
+ * Scores and sums are fp32, the sum in an order that follows from the batch
+ * (the same call gives the same bits).  What an invisible token holds has no
+ * effect; a row that sees nothing (lse -inf) adds nothing; a NaN among the
+ * visible keys, in q or in lse makes the page's mass NaN.
+ *
+ *   q, scale, window, sinks, row0, ell, len, table, pool  as in
+ *        dspark_cache_attention (values are not read)
+ *   lse  [rows][Hq] f32, dspark_cache_attention's
+ *   keep finite and >= 0
+ *   mass [R][max_pages] f32 in/out
+ *
+ * Limits: as dspark_cache_attention.
+ */
+dspark_status dspark_cache_weigh(int fmt, int R, int gamma, int Hq, int Hkv, int D, int P, int n_pages,
+                                 int max_pages, const void* q, float scale, int window, int sinks,
+                                 const float* lse, const int32_t* row0, const int32_t* ell, const int32_t* len,
+                                 const int32_t* table, const void* pool, float keep, float* mass, void* stream);
+
+/*
  * Ownership of the pages.  Per pool (the layers of a model share it):
- *   table [R][max_pages] i32   page ids, -1 = none
+ *   table [R][max_pages] i32   page ids, -1 = none, -2 = evicted
  *   len   [R] i32              committed tokens
  *   ref   [n_pages] i32        table entries that name the page
  *   bits  [ceil(n_pages / 32)] u32, bit p % 32 of word p / 32 set iff ref[p]
@@ -192,7 +244,7 @@ dspark_status dspark_cache_reset(int R, int n_pages, int max_pages, int32_t* tab
 /*
  * dspark_cache_reserve — pages for rows len[r] .. len[r] + ell[r].
  *
- * Entries that are -1 get new pages.  If the page that holds token len[r] - 1
+ * Entries that are no page get new pages.  If the page that holds token len[r] - 1
  * is also to be written (len[r] % P != 0) and other requests hold it too, r
  * gets a copy of it instead: pairs gets (old, new), and the old page loses a
  * reference; of several such requests of one call the last keeps the old page
@@ -237,6 +289,24 @@ dspark_status dspark_cache_commit(int R, int gamma, int P, int n_pages, int max_
 dspark_status dspark_cache_fork(int R, int P, int n_pages, int max_pages, const int32_t* from, int32_t* len,
                                 int32_t* table, int32_t* ref, uint32_t* bits, void* ws, size_t ws_bytes,
                                 void* stream);
+
+/*
+ * dspark_cache_evict — request r keeps at most budget[r] pages of committed
+ * tokens: while it has more, the page of least mass among those it may lose is
+ * let go (ties: the lower entry; NaN counts as the largest), its entry becomes
+ * -2 and its mass 0.  It may lose a page whose tokens are all at or past
+ * `sinks` and before len[r] - recent; if these are too few, all of them go.
+ * A page that other requests hold stays theirs.  budget[r] < 0 leaves r alone.
+ * No page may be reserved and not committed.
+ *
+ *   mass [R][max_pages] f32 in/out (dspark_cache_weigh's, or any ranking)
+ *   budget [R] i32; freed [R] i32 out or NULL: how many pages r lost
+ *
+ * Limits: sinks >= 0, recent >= 0.
+ */
+dspark_status dspark_cache_evict(int R, int P, int n_pages, int max_pages, int sinks, int recent,
+                                 const int32_t* budget, const int32_t* len, float* mass, int32_t* table,
+                                 int32_t* ref, uint32_t* bits, int32_t* freed, void* stream);
 
 /*
  * dspark_cache_compact — moves pages so that the U pages in use are 0 .. U-1:

@@ -68,6 +68,99 @@ def quantise_v(v):
     return np.where(bad, np.nan, E2M1[idx] * unit * np.sign(v))
 
 
+# e4m3: 0x00 .. 0x7E are the magnitudes in order, 0x7F is NaN
+E4M3 = np.array([m * 2.0 ** -9 for m in range(8)] + [(8 + m) * 2.0 ** (e - 10) for e in range(1, 16) for m in range(8)])
+E4M3[127] = np.nan
+FP8 = 4
+LOW8, HIGH8 = -117, 119
+
+
+def codes8(y):
+    """Codes of y: nearest, ties to the even code, NaN where y is not finite;
+    larger values get the largest code."""
+    y = np.asarray(y, np.float64)
+    bad = ~np.isfinite(y)
+    a = np.minimum(np.abs(np.where(bad, 0, y)), 448.0)
+    i = np.searchsorted(E4M3[:127], a)                   # E4M3[i - 1] < a <= E4M3[i]
+    low = np.maximum(i - 1, 0)
+    up, down = E4M3[i] - a, a - E4M3[low]
+    c = np.where((up < down) | ((up == down) & (i % 2 == 0)), i, low)
+    return (np.where(bad, 127, c) | np.where(np.signbit(y), 128, 0)).astype(np.uint8)
+
+
+def values8(c):
+    return np.where(c & 128, -1.0, 1.0) * E4M3[c & 127]
+
+
+def join8(codes, e, new):
+    """A block takes tokens in: codes [old][D] under the scale 2^e (old = 0: e
+    does not matter), new [n][D].  Returns codes [old + n][D] and the exponent."""
+    top = np.abs(np.where(np.isfinite(new), new, 0)).max(initial=0.0)
+    need = LOW8
+    while need < HIGH8 and top > 448 * 2.0 ** need:
+        need += 1
+    to = need if len(codes) == 0 else max(e, need)
+    old = codes if len(codes) == 0 or to == e else codes8(values8(codes) * 2.0 ** (e - to))
+    return np.concatenate([old, codes8(np.asarray(new) * 2.0 ** -to)]), to
+
+
+class Rows8:
+    """One request's tokens of one head in 8 bits: blocks of 16 with their
+    codes and exponent, K or V."""
+
+    def __init__(self, D):
+        self.codes, self.e = np.zeros((0, D), np.uint8), []
+
+    def append(self, at, new):
+        """Rows `new` at positions at .. (those that were there are rolled back)."""
+        self.codes = self.codes[:at]
+        self.e = self.e[:-(-at // 16)]
+        for a in range(at // 16 * 16, at + len(new), 16):
+            lo, hi = max(a, at), min(a + 16, at + len(new))
+            c, e = join8(self.codes[a:], self.e[a // 16] if lo > a else 0, new[lo - at:hi - at])
+            self.codes = np.concatenate([self.codes[:a], c])
+            self.e = self.e[:a // 16] + [e]
+
+    def values(self):
+        e = np.repeat(np.array(self.e, np.float64), 16)[:len(self.codes)]
+        return values8(self.codes) * np.exp2(e)[:, None]
+
+
+def write_pages8(ks, vs, table, P, pool):
+    """Rows8 of every head into 8-bit pages, uint8 [n_pages][bytes]."""
+    H, D = len(ks), ks[0].codes.shape[1]
+    hb, E = pool.shape[1] // H, D // 32
+    for h in range(H):
+        for t in range(len(ks[h].codes)):
+            head = pool[table[t // P]][h * hb:(h + 1) * hb]
+            i, b, u = t % P, t % P // 16, t % 16
+            head[b * 16 * D:(b + 1) * 16 * D].reshape(D // 16, 16, 16)[:, u] = ks[h].codes[t].reshape(D // 16, 16)
+            v = head[P * D + b * 16 * D:P * D + (b + 1) * 16 * D].reshape(2, 32, E, 8)
+            v[u // 8, :, :, u % 8] = vs[h].codes[t].reshape(E, 32).T
+            head[2 * P * D + b] = ks[h].e[t // 16] + 127
+            head[2 * P * D + 8 + b] = vs[h].e[t // 16] + 127
+
+
+def weigh(q, lse, k, pos, scale, window, sinks, P, have=None):
+    """Attention weights of every page's tokens: q [rows][Hq][D] at positions
+    pos with log-sums lse [rows][Hq]; k [tokens][Hkv][D].  Returns [pages]."""
+    rows, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    j = np.arange(k.shape[0])
+    mass = np.zeros(-(-k.shape[0] // P))
+    for i in range(rows):
+        see = j <= pos[i]
+        if window:
+            see &= (j > pos[i] - window) | (j < sinks)
+        if have is not None:
+            see &= have
+        for h in range(Hq):
+            if see.any() and lse[i, h] != -np.inf:
+                s = k[see, h // G].astype(np.float64) @ q[i, h].astype(np.float64) * scale
+                np.add.at(mass, j[see] // P, np.exp(s - float(lse[i, h])))
+    return mass
+
+
 def attention(q, k, v, pos, scale, window, sinks, have=None):
     """q [rows][Hq][D] at positions pos; k, v [tokens][Hkv][D]; have [tokens]:
     False where the token has no page.  Returns out, lse."""
@@ -217,3 +310,19 @@ class Pages:
         to = dict(zip(src, dst))
         self.table = np.vectorize(lambda p: to.get(p, p), otypes=[np.int64])(self.table)
         return list(zip(src, dst))
+
+    def evict(self, mass, budget, sinks, recent):
+        """mass [R][M] (changed in place).  Returns how many pages each request
+        lost; an evicted entry is -2."""
+        freed = []
+        for r in range(self.R):
+            n = int(self.len[r])
+            held = [i for i in range(min(-(-n // self.P), self.M)) if self.table[r, i] >= 0]
+            may = [i for i in held if i * self.P >= sinks and (i + 1) * self.P <= n - recent]
+            k = 0 if budget[r] < 0 else min(max(len(held) - int(budget[r]), 0), len(may))
+            # NaN last, equal ones (zeros of either sign too) by entry
+            for i in sorted(may, key=lambda i: (np.isnan(mass[r, i]), 0 if np.isnan(mass[r, i]) else mass[r, i], i))[:k]:
+                self.table[r, i] = -2
+                mass[r, i] = 0
+            freed.append(k)
+        return freed

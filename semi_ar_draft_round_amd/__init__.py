@@ -11,7 +11,8 @@ _BINDING_NAMES = (
     "dspark_workspace_size", "dspark_status_string", "load_library", "DSparkError",
     "dspark_cache_append", "dspark_cache_attention", "dspark_cache_read", "dspark_cache_reset",
     "dspark_cache_reserve", "dspark_cache_commit", "dspark_cache_fork", "dspark_cache_compact", "dspark_cache_copy",
-    "dspark_cache_page_bytes", "dspark_cache_workspace_size",
+    "dspark_cache_weigh", "dspark_cache_evict", "dspark_cache_page_bytes", "dspark_cache_workspace_size",
+    "dspark_logits", "dspark_logits_prompt", "dspark_logits_commit",
 )
 
 

@@ -57,7 +57,7 @@ _SIGNATURES = {
 EXPORTED = tuple(_SIGNATURES)
 
 # include/dspark_cache.h
-CACHE_BF16, CACHE_FP4 = 1, 2
+CACHE_BF16, CACHE_FP4, CACHE_FP8 = 1, 2, 4
 CACHE_WS_ATTENTION, CACHE_WS_RESERVE, CACHE_WS_FORK, CACHE_WS_COMPACT = 0, 1, 2, 3
 ENOPAGES = 7   # device status of dspark_cache_reserve
 
@@ -70,6 +70,8 @@ _CACHE_SIGNATURES = {
     "dspark_cache_append": [_I] * 9 + [_P, _L, _P, _L, _P, _L, _P, _P, _F, _P, _I, _I] + [_P] * 7,
     "dspark_cache_attention": [_I] * 9 + [_P, _F, _I, _I] + [_P] * 8 + [_SZ, _P],
     "dspark_cache_read": [_I] * 8 + [_P] * 7,
+    "dspark_cache_weigh": [_I] * 9 + [_P, _F, _I, _I] + [_P] * 6 + [_F, _P, _P],
+    "dspark_cache_evict": [_I] * 6 + [_P] * 8,
     "dspark_cache_reset": [_I, _I, _I] + [_P] * 5,
     "dspark_cache_reserve": [_I] * 5 + [_P] * 10 + [_SZ, _P],
     "dspark_cache_commit": [_I] * 7 + [_P] * 7,
@@ -78,6 +80,14 @@ _CACHE_SIGNATURES = {
     "dspark_cache_copy": [_I, _L, _L, _I, _P, _P, _I, _P, _P],
 }
 CACHE_EXPORTED = tuple(_CACHE_SIGNATURES)
+
+# include/dspark_logits.h
+_LOGITS_SIGNATURES = {
+    "dspark_logits": [_I] * 4 + [_P] * 9 + [_I] + [_P] * 5,
+    "dspark_logits_prompt": [_I, _I, _L] + [_P] * 5,
+    "dspark_logits_commit": [_I, _I, _I] + [_P] * 6,
+}
+LOGITS_EXPORTED = tuple(_LOGITS_SIGNATURES)
 
 
 class DSparkError(RuntimeError):
@@ -94,7 +104,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: run `python -m semi_ar_draft_round_amd.build` first")
     lib = ctypes.CDLL(path)
-    for name, args in (_SIGNATURES | _CACHE_SIGNATURES).items():
+    for name, args in (_SIGNATURES | _CACHE_SIGNATURES | _LOGITS_SIGNATURES).items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
@@ -729,6 +739,32 @@ def dspark_cache_read(pool, table, start, count, T, *, fmt, page, heads_kv, dim,
     return k, v
 
 
+def dspark_cache_weigh(q, lse, pool, table, length, ell, gamma, mass, *, keep=1.0, fmt, page, heads_kv, scale=None,
+                       window=0, sinks=0, row0=None):
+    """mass [R][max_pages] float32 <- keep * mass + the attention weights that
+    each page's tokens get from the rows, summed over rows and heads; q, scale,
+    window, sinks and lse [rows][Hq] are dspark_cache_attention's.  Returns
+    mass."""
+    dev = q.get_device()
+    if q.dim() != 3:
+        raise ValueError("q must be [rows][heads][dim]")
+    rows, Hq, D = q.shape
+    R, max_pages, p_row0, p_ell, p_len, p_table = _batch(table, length, ell, gamma, row0, rows, dev)
+    p_q = _need(q, "q", (rows, Hq, D), _BF, dev)
+    p_lse = _need(lse, "lse", (rows, Hq), torch.float32, dev)
+    n_pages, p_pool = _pool(pool, fmt, heads_kv, D, page, dev)
+    p_mass = _need(mass, "mass", (R, max_pages), torch.float32, dev)
+    _int32(window, sinks)
+    stream = _raw_stream(dev)
+    if rows == 0:
+        return mass
+    st = load_library().dspark_cache_weigh(fmt, R, gamma, Hq, heads_kv, D, page, n_pages, max_pages, p_q,
+                                           D ** -0.5 if scale is None else scale, window, sinks, p_lse, p_row0, p_ell,
+                                           p_len, p_table, p_pool, keep, p_mass, stream)
+    _raise("dspark_cache_weigh", st)
+    return mass
+
+
 def _pages(table, length, ref, bits):
     """R, max_pages, n_pages, the device, and the addresses of the four."""
     dev = table.get_device()
@@ -794,6 +830,21 @@ def dspark_cache_fork(table, length, ref, bits, parent, *, page, ws=None):
     _raise("dspark_cache_fork", st)
 
 
+def dspark_cache_evict(table, length, ref, bits, mass, budget, *, page, sinks=0, recent=0, freed=None):
+    """Request r lets go of its pages of least mass until budget[r] (int32; < 0:
+    no limit) are left, never of the first `sinks` and the last `recent` tokens;
+    their table entries become -2.  Returns freed [R] int32: how many went."""
+    R, max_pages, n_pages, dev, p_table, p_len, p_ref, p_bits = _pages(table, length, ref, bits)
+    _int32(page, sinks, recent)
+    freed = torch.empty(R, dtype=_I32, device=table.device) if freed is None else freed
+    p_mass = _need(mass, "mass", (R, max_pages), torch.float32, dev)
+    p_budget, p_freed = _need(budget, "budget", (R,), _I32, dev), _need(freed, "freed", (R,), _I32, dev)
+    st = load_library().dspark_cache_evict(R, page, n_pages, max_pages, sinks, recent, p_budget, p_len, p_mass, p_table,
+                                           p_ref, p_bits, p_freed, _raw_stream(dev))
+    _raise("dspark_cache_evict", st)
+    return freed
+
+
 def dspark_cache_compact(table, ref, bits, pairs=None, n_pairs=None, ws=None):
     """Pages in use to the low ids; returns pairs [n_pages // 2 or more][2] and
     n_pairs [1] for dspark_cache_copy."""
@@ -825,3 +876,84 @@ def dspark_cache_copy(pool, pairs, n_pairs):
     st = load_library().dspark_cache_copy(layers, n_pages * nb, nb, n_pages, p_pairs, p_n, pairs.shape[0], p_pool,
                                           _raw_stream(dev))
     _raise("dspark_cache_copy", st)
+
+
+# ---------------------------------------------------------------- include/dspark_logits.h
+
+def _state(state, R, V, dev):
+    if state.dtype is not torch.int16:
+        raise ValueError(f"state: dtype {state.dtype} is not int16 (bit 15: in the prompt; the others: a count)")
+    return _need(state, "state", (R, V), torch.int16, dev)
+
+
+def _drafts(x, R, gamma, dev):
+    """The drafts [R][gamma], None where there are none."""
+    return None if x is None or gamma == 0 else _need(x, "x", (R, gamma), _I32, dev)
+
+
+def dspark_logits(logits, state, ell, gamma, x0, x=None, *, row0=None, repetition=None, presence=None, frequency=None,
+                  bias_tok=None, bias=None, mask=None, out=None):
+    """out (a new tensor, or given, also logits itself; rows of nobody are not
+    written): the rows' logits with penalties, biases and masks.  logits [rows][V] or, without row0, [R][gamma +
+    1][V]; state [R][V] int16 (None: no penalties); x0 [R], x [R][gamma] int32;
+    repetition, presence, frequency [R] float32; bias_tok [R][n] int32 with bias
+    [R][n] float32; mask [rows][ceil(V / 32)] int32, bit v % 32 of word v / 32
+    set where v is allowed."""
+    dev = logits.get_device()
+    if logits.dim() not in (2, 3) or (logits.dim() == 3 and row0 is not None):
+        raise ValueError("logits must be [rows][V], or [R][gamma + 1][V] without row0")
+    R, V = ell.shape[0], logits.shape[-1]
+    rows = logits.numel() // V if V else 0
+    _int32(gamma)
+    if row0 is None and rows != R * (gamma + 1):
+        raise ValueError(f"{rows} rows: without row0 there are R * (gamma + 1) = {R * (gamma + 1)}")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits: dtype {logits.dtype} is neither bfloat16 nor float32")
+    p_in = _need(logits, "logits", logits.shape, logits.dtype, dev)
+    p_ell = _need(ell, "ell", (R,), _I32, dev)
+    p_row0 = None if row0 is None else _need(row0, "row0", (R,), _I32, dev)
+    p_state = None if state is None else _state(state, R, V, dev)
+    p_x0 = None if x0 is None else _need(x0, "x0", (R,), _I32, dev)
+    p_x = _drafts(x, R, gamma, dev)
+    per = [None if t is None else _need(t, n, (R,), torch.float32, dev)
+           for t, n in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency"))]
+    nb, p_tok, p_bias = 0, None, None
+    if bias_tok is not None:
+        nb = bias_tok.shape[-1]
+        p_tok = _need(bias_tok, "bias_tok", (R, nb), _I32, dev)
+        p_bias = _need(bias, "bias", (R, nb), torch.float32, dev)
+    p_mask = None if mask is None else _need(mask, "mask", (rows, (V + 31) // 32), _I32, dev)
+    out = torch.empty_like(logits) if out is None else out
+    p_out = _need(out, "out", logits.shape, logits.dtype, dev)
+    stream = _raw_stream(dev)
+    if rows == 0:
+        return out
+    st = load_library().dspark_logits(_dt(logits), R, gamma, V, p_in, p_row0, p_ell, p_x0, p_x, p_state, *per, nb,
+                                      p_tok, p_bias, p_mask, p_out, stream)
+    _raise("dspark_logits", st)
+    return out
+
+
+def dspark_logits_prompt(state, tokens, start, count):
+    """Slot r of state [R][V] int16 becomes the history of the prompt
+    tokens[start[r]] .. of count[r] tokens (< 0: the slot stays as it is)."""
+    dev = state.get_device()
+    R, V = state.shape
+    p_tokens = _need(tokens, "tokens", (tokens.shape[0],), _I32, dev)
+    st = load_library().dspark_logits_prompt(R, V, tokens.shape[0], p_tokens if tokens.shape[0] else None,
+                                             _need(start, "start", (R,), _I32, dev),
+                                             _need(count, "count", (R,), _I32, dev), _state(state, R, V, dev),
+                                             _raw_stream(dev))
+    _raise("dspark_logits_prompt", st)
+
+
+def dspark_logits_commit(state, ell, n_acc, x0, x=None):
+    """The anchors and the accepted drafts of a round's requests (ell[r] >= 0)
+    join the history."""
+    dev = state.get_device()
+    R, V = state.shape
+    gamma = 0 if x is None else x.shape[1]
+    st = load_library().dspark_logits_commit(R, gamma, V, _need(ell, "ell", (R,), _I32, dev),
+                                             _need(n_acc, "n_acc", (R,), _I32, dev), _need(x0, "x0", (R,), _I32, dev),
+                                             _drafts(x, R, gamma, dev), _state(state, R, V, dev), _raw_stream(dev))
+    _raise("dspark_logits_commit", st)

@@ -10,6 +10,9 @@ and calls the entry points in the order a round needs:
         o, _ = cache.attend(layer, q, ...)
     cache.commit(d.n_acc)                         # after dspark_verify
 
+With a budget of pages, attend also weighs the pages and commit lets go of
+those that got least attention.
+
 Nothing is allocated after construction except output tensors and the
 attention's workspace where the caller does not pass them, from torch's
 allocator, so a round can be captured in a HIP graph.  All calls run on the
@@ -23,12 +26,26 @@ import torch
 from . import binding as B
 
 
+def rows_of_parents(t, parent, empty: bool):
+    """Row r of the result: row parent[r] of t; for parent[r] = -1 zeros if
+    `empty`, else t's own row, as for parents that are no row."""
+    n = t.shape[0]
+    own = torch.arange(n, dtype=parent.dtype, device=parent.device)
+    rows = t[torch.where((parent >= 0) & (parent < n), parent, own).long()]
+    return torch.where((parent == -1).view(-1, *[1] * (t.dim() - 1)), torch.zeros_like(rows), rows) if empty else rows
+
+
 class PagedCache:
     def __init__(self, layers: int, slots: int, max_tokens: int, n_pages: int, heads_kv: int, dim: int, page: int = 64,
-                 fmt: int = B.CACHE_BF16, window: int = 0, sinks: int = 0, device="cuda:0"):
+                 fmt: int = B.CACHE_BF16, window: int = 0, sinks: int = 0, device="cuda:0", budget: int | None = None,
+                 fade: float = 1.0, keep_first: int = 0, keep_last: int = 0):
         """slots: requests; max_tokens: the longest a request may get (its
         rows of a round included); window, sinks: the attention's (0: none),
-        so that commit can release what no later row sees."""
+        so that commit can release what no later row sees.  budget: pages a
+        request may keep after a commit (None: all; self.budget [slots] holds
+        it, so that requests can have their own): those whose tokens got the
+        least attention go, never the first keep_first and the last keep_last
+        tokens'; earlier rounds count `fade` times as much with every round."""
         dev = torch.device(device)
         nb = B.dspark_cache_page_bytes(fmt, heads_kv, dim, page)
         if nb == 0 or layers < 1 or slots < 1 or max_tokens < 1 or n_pages < 1:
@@ -36,6 +53,10 @@ class PagedCache:
                              f"{page} tokens, {heads_kv} heads of {dim}, format {fmt}")
         if not 0 <= window <= 0x7FFFFFFF or not 0 <= sinks <= 0x7FFFFFFF:
             raise ValueError("window and sinks must be 0 .. 2^31 - 1")
+        if budget is not None and (not 0 <= budget <= 0x7FFFFFFF or not 0 <= fade < float("inf")):
+            raise ValueError("budget must be 0 .. 2^31 - 1 pages, fade finite and not negative")
+        if not 0 <= keep_first <= 0x7FFFFFFF or not 0 <= keep_last <= 0x7FFFFFFF:
+            raise ValueError("keep_first and keep_last must be 0 .. 2^31 - 1")
         self.heads_kv, self.dim, self.page, self.fmt = heads_kv, dim, page, fmt
         self.window, self.sinks = window, sinks
         i32 = dict(dtype=torch.int32, device=dev)
@@ -54,10 +75,18 @@ class PagedCache:
         self.ws = torch.empty(max(1, *(B.dspark_cache_workspace_size(k, slots, 0, max_pages, n_pages) for k in kinds)),
                               dtype=torch.uint8, device=dev)
         self.gamma = 0
+        self.fade, self.keep_first, self.keep_last = fade, keep_first, keep_last
+        self.budget = self.mass = self.freed = None
+        if budget is not None:
+            self.budget = torch.full((slots,), budget, **i32)
+            self.mass = torch.zeros((slots, max_pages), dtype=torch.float32, device=dev)
+            self.freed = torch.zeros(slots, **i32)   # pages that the last commit let go
         self.reset()
 
     def reset(self):
         B.dspark_cache_reset(self.table, self.length, self.ref, self.bits)
+        if self.mass is not None:
+            self.mass.zero_()
 
     def reserve(self, ell, gamma: int):
         """Pages for every request's ell[r] + 1 rows (-1: none), shared pages
@@ -81,19 +110,34 @@ class PagedCache:
 
     def attend(self, layer: int, q, *, scale=None, row0=None, out=None, lse=None, ws=None):
         """The reserved rows' attention over layer's pages
-        (dspark_cache_attention with the cache's window)."""
-        return B.dspark_cache_attention(q, self.pool[layer], self.table, self.length, self.ell, self.gamma,
-                                        fmt=self.fmt, page=self.page, heads_kv=self.heads_kv, scale=scale,
-                                        window=self.window, sinks=self.sinks, row0=row0, out=out, lse=lse, ws=ws)
+        (dspark_cache_attention with the cache's window).  With a budget the
+        pages are weighed too (the mass of earlier rounds fades with layer 0),
+        and lse is made if it is not given."""
+        if self.mass is not None and lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        same = dict(fmt=self.fmt, page=self.page, heads_kv=self.heads_kv, scale=scale, window=self.window,
+                    sinks=self.sinks, row0=row0)
+        out, lse = B.dspark_cache_attention(q, self.pool[layer], self.table, self.length, self.ell, self.gamma, out=out,
+                                            lse=lse, ws=ws, **same)
+        if self.mass is not None:
+            B.dspark_cache_weigh(q, lse, self.pool[layer], self.table, self.length, self.ell, self.gamma, self.mass,
+                                 keep=self.fade if layer == 0 else 1.0, **same)
+        return out, lse
 
     def commit(self, n_acc):
-        """Keep the anchor and the first n_acc[r] drafts of the reserved rows."""
+        """Keep the anchor and the first n_acc[r] drafts of the reserved rows;
+        with a budget, let go of the pages past it (self.freed of them)."""
         B.dspark_cache_commit(self.table, self.length, self.ref, self.bits, self.ell, n_acc, self.gamma,
                               page=self.page, window=self.window, sinks=self.sinks)
+        if self.budget is not None:
+            B.dspark_cache_evict(self.table, self.length, self.ref, self.bits, self.mass, self.budget, page=self.page,
+                                 sinks=self.keep_first, recent=self.keep_last, freed=self.freed)
 
     def fork(self, parent):
         """Request r takes over parent[r]'s tokens, shared (r: stays; -1: empty)."""
         B.dspark_cache_fork(self.table, self.length, self.ref, self.bits, parent, page=self.page, ws=self.ws)
+        if self.mass is not None:
+            self.mass.copy_(rows_of_parents(self.mass, parent, empty=True))
 
     def compact(self):
         """Pages in use to the low ids of every layer's pool."""

@@ -1,4 +1,4 @@
-// The paged cache's shapes, page layouts and 4-bit codes (include/dspark_cache.h).
+// The paged cache's shapes, page layouts, 4-bit and 8-bit codes (include/dspark_cache.h).
 #pragma once
 
 #include "common.hpp"
@@ -53,6 +53,24 @@ struct PageLayout<DSPARK_CACHE_FP4, D> {
   static __device__ int64_t v_scale(int P, int t) { return static_cast<int64_t>(P) * (D + E) + t * 4LL; }
 };
 
+template <int D>
+struct PageLayout<DSPARK_CACHE_FP8, D> {
+  static constexpr int E = D / 32;
+  static __host__ __device__ int64_t head_bytes(int P) { return 2LL * P * D + 16; }
+  // the 16 bytes of dims 16*g .. of token t
+  static __device__ int64_t k(int P, int t, int g) {
+    return static_cast<int64_t>(t >> 4) * (16 * D) + (g * 16 + (t & 15)) * 16;
+  }
+  // tokens 8*(t/8) .. of dim d: 8 bytes
+  static __device__ int64_t v(int P, int t, int d) {
+    return static_cast<int64_t>(P) * D + static_cast<int64_t>(t >> 4) * (16 * D) +
+           ((((t >> 3) & 1) * 32 + (d & 31)) * E + (d >> 5)) * 8;
+  }
+  // a byte for each block of 16 tokens
+  static __device__ int64_t k_scale(int P, int t) { return 2LL * P * D + (t >> 4); }
+  static __device__ int64_t v_scale(int P, int t) { return 2LL * P * D + 8 + (t >> 4); }
+};
+
 // Rows of request r this time, 0 .. gamma + 1, from a device value.
 __device__ __forceinline__ int rows_of(int ell, int gamma) { return ell < 0 ? 0 : (ell > gamma ? gamma : ell) + 1; }
 
@@ -88,6 +106,22 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w, float scale) {
 __device__ __forceinline__ float k_scale_value(uint32_t b) { return __uint_as_float(b << 23); }
 __device__ __forceinline__ u32x4 fp4_octet(uint32_t w, float scale) {
   return u32x4{fp4_pair<0>(w, scale), fp4_pair<1>(w, scale), fp4_pair<2>(w, scale), fp4_pair<3>(w, scale)};
+}
+
+// Two e4m3 codes (half SEL of w) times 2^(exponent of scale) as bf16, exact,
+// and eight of them (a scale byte's 2^(b - 127) as above).
+template <bool SEL>
+__device__ __forceinline__ uint32_t fp8_pair(uint32_t w, float scale) {
+  union {
+    bf16x2 b;
+    uint32_t u;
+  } r;
+  r.b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, SEL);
+  return r.u;
+}
+__device__ __forceinline__ u32x4 fp8_octet(uint32_t lo, uint32_t hi, float scale) {
+  return u32x4{fp8_pair<false>(lo, scale), fp8_pair<true>(lo, scale), fp8_pair<false>(hi, scale),
+               fp8_pair<true>(hi, scale)};
 }
 
 // The value of another lane by a fixed pattern, without the way through LDS

@@ -20,7 +20,15 @@ hipError_t cache_attention_launch(int fmt, int R, int gamma, int Hq, int Hkv, in
                                   int max_pages, const void* q, float scale, int window, int sinks,
                                   const int32_t* row0, const int32_t* ell, const int32_t* len, const int32_t* table,
                                   const void* pool, void* out, float* lse, void* ws, hipStream_t s);
+// cache_weigh.hip
+hipError_t cache_weigh_launch(int fmt, int R, int gamma, int Hq, int Hkv, int D, int P, int n_pages, int max_pages,
+                              const void* q, float scale, int window, int sinks, const float* lse,
+                              const int32_t* row0, const int32_t* ell, const int32_t* len, const int32_t* table,
+                              const void* pool, float keep, float* mass, hipStream_t s);
 // cache_pages.hip
+hipError_t cache_evict_launch(int R, int P, int n_pages, int max_pages, int sinks, int recent, const int32_t* budget,
+                              const int32_t* len, float* mass, int32_t* table, int32_t* ref, uint32_t* bits,
+                              int32_t* freed, hipStream_t s);
 hipError_t cache_reset_launch(int R, int n_pages, int max_pages, int32_t* table, int32_t* len, int32_t* ref,
                               uint32_t* bits, hipStream_t s);
 hipError_t cache_reserve_launch(int R, int gamma, int P, int n_pages, int max_pages, const int32_t* ell,
@@ -38,7 +46,7 @@ hipError_t cache_copy_launch(int layers, int64_t layer_bytes, int64_t page_bytes
 
 namespace {
 
-bool format_ok(int fmt) { return fmt == DSPARK_CACHE_BF16 || fmt == DSPARK_CACHE_FP4; }
+bool format_ok(int fmt) { return fmt == DSPARK_CACHE_BF16 || fmt == DSPARK_CACHE_FP4 || fmt == DSPARK_CACHE_FP8; }
 bool page_ok(int P) { return P == 16 || P == 32 || P == 64 || P == 128; }
 bool dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 bool heads_ok(int H) { return H >= 1 && H <= kCacheMaxHeads; }
@@ -67,6 +75,7 @@ extern "C" {
 
 size_t dspark_cache_page_bytes(int fmt, int Hkv, int D, int P) {
   if (!format_ok(fmt) || !heads_ok(Hkv) || !dim_ok(D) || !page_ok(P)) return 0;
+  if (fmt == DSPARK_CACHE_FP8) return (2 * static_cast<size_t>(P) * D + 16) * Hkv;
   const size_t token = fmt == DSPARK_CACHE_BF16 ? 4 * static_cast<size_t>(D) : static_cast<size_t>(D) + D / 32 + 4;
   return token * P * Hkv;
 }
@@ -151,6 +160,35 @@ dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, in
   if (st != DSPARK_OK) return st;
   return launched(cache_read_launch(fmt, R, T, Hkv, D, P, n_pages, max_pages, start, count, table, pool, k, v,
                                     static_cast<hipStream_t>(stream)));
+}
+
+dspark_status dspark_cache_weigh(int fmt, int R, int gamma, int Hq, int Hkv, int D, int P, int n_pages,
+                                 int max_pages, const void* q, float scale, int window, int sinks, const float* lse,
+                                 const int32_t* row0, const int32_t* ell, const int32_t* len, const int32_t* table,
+                                 const void* pool, float keep, float* mass, void* stream) {
+  if (!format_ok(fmt)) return DSPARK_EDTYPE;
+  if (!batch_ok(R, gamma) || !heads_ok(Hq) || !heads_ok(Hkv) || Hq % Hkv != 0 || !dim_ok(D) || !page_ok(P) ||
+      !pages_ok(R, n_pages, max_pages))
+    return DSPARK_EINVAL;
+  if (window < 0 || sinks < 0 || !(fabsf(scale) <= 0x1p126f)) return DSPARK_EINVAL;  // times log2 e: still finite
+  if (!(keep >= 0.f) || isinf(keep)) return DSPARK_EINVAL;
+  if (!q || !lse || !ell || !len || !table || !pool || !mass) return DSPARK_EINVAL;
+  if (!aligned(static_cast<const char*>(q), static_cast<const char*>(pool))) return DSPARK_EINVAL;
+  dspark_status st = check_device();
+  if (st != DSPARK_OK) return st;
+  return launched(cache_weigh_launch(fmt, R, gamma, Hq, Hkv, D, P, n_pages, max_pages, q, scale, window, sinks, lse,
+                                     row0, ell, len, table, pool, keep, mass, static_cast<hipStream_t>(stream)));
+}
+
+dspark_status dspark_cache_evict(int R, int P, int n_pages, int max_pages, int sinks, int recent,
+                                 const int32_t* budget, const int32_t* len, float* mass, int32_t* table,
+                                 int32_t* ref, uint32_t* bits, int32_t* freed, void* stream) {
+  if (!page_ok(P) || !pages_ok(R, n_pages, max_pages) || sinks < 0 || recent < 0) return DSPARK_EINVAL;
+  if (!budget || !len || !mass || !table || !ref || !bits) return DSPARK_EINVAL;
+  dspark_status st = check_device();
+  if (st != DSPARK_OK) return st;
+  return launched(cache_evict_launch(R, P, n_pages, max_pages, sinks, recent, budget, len, mass, table, ref, bits,
+                                     freed, static_cast<hipStream_t>(stream)));
 }
 
 dspark_status dspark_cache_reset(int R, int n_pages, int max_pages, int32_t* table, int32_t* len, int32_t* ref,

@@ -17,132 +17,11 @@
 // packed rows, 56 query heads, 12.3 us (15.1 with the sums over a head and the
 // rotation's partners through LDS instead of lane patterns), of which V of
 // groups that are not whole, in 2-byte stores, is 1.8; 4 x 512 rows 14.5 us.
-#include "cache.hpp"
+#include "cache_rows.hpp"
 
 namespace dspark {
 
 namespace {
-
-constexpr int kGroup = 8;  // tokens of a V word
-constexpr int kThreads = 256;
-
-struct AppendArgs {
-  int R, gamma, Hq, Hkv, P, n_pages, max_pages, groups;
-  const uint16_t *q, *k, *v;
-  int64_t ldq, ldk, ldv;
-  const uint16_t *wq, *wk;
-  float eps;
-  const double* freq;
-  int rot, adjacent;
-  const int32_t *row0, *ell, *len, *table;
-  uint16_t* q_out;
-  char* pool;
-  int64_t page_bytes;
-  int page_shift;
-  float per_q, per_k, per_half;  // 1 / Hq, 1 / Hkv, 1 / (rot / 2)
-};
-
-// x / y for 0 <= x < 2^14, 1 <= y <= 2^10 and inv = 1 / y in fp32: x + 1/2 is
-// at least 1 / (2 y) from a multiple of y, far more than the product's error.
-__device__ __forceinline__ int small_quotient(int x, float inv) {
-  return static_cast<int>((static_cast<float>(x) + 0.5f) * inv);
-}
-
-// f over the values of L = 4, 8, 16 or 32 neighbouring lanes, the same in each
-// (f commutes, so also the same bits).
-template <int L, typename T, typename F>
-__device__ __forceinline__ T over_lanes(T x, F f) {
-  x = f(x, lane_pattern<kSwap1>(x));
-  x = f(x, lane_pattern<kSwap2>(x));
-  if constexpr (L > 4) x = f(x, lane_pattern<kMirror8>(x));
-  if constexpr (L > 8) x = f(x, lane_pattern<kMirror16>(x));
-  if constexpr (L > 16) x = f(x, __shfl_xor(x, 16));
-  return x;
-}
-
-__device__ __forceinline__ float inv_sqrt(float x) { return rsqrtf(x); }
-__device__ __forceinline__ double inv_sqrt(double x) { return 1.0 / sqrt(x); }
-
-// The norm and the rotation of one head, 8 dims per lane, in the type T.
-// li: the lane's place in the head; w: the norm's weights of its dims; cs:
-// cosine and sine of pair i at 2 i.
-template <typename T, int D>
-__device__ __forceinline__ void norm_rotate(T (&x)[8], int li, bool norm, const u32x4& w, float eps, int rot,
-                                            bool adjacent, const T* cs) {
-  constexpr int L = D / 8;
-  if (norm) {
-    T ss = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-    ss = over_lanes<L>(ss, [](T p, T q) { return p + q; });
-    T s = inv_sqrt(ss * static_cast<T>(1.0 / D) + static_cast<T>(eps));
-    if constexpr (sizeof(T) == 4) {
-      // a sum of squares that fp32 does not hold, or not whole (an |x| past
-      // 2^60, or a sum below 2^-96): the head again in fp64, a rare branch of
-      // the wave; its test costs 0.2 us of 12.2 for 128 x up to 17 packed rows
-      const bool in_range = __float_as_uint(ss) - 0x0F800000u < 0x7B800000u - 0x0F800000u;  // 2^-96 .. 2^120
-      if (__builtin_expect(__any(!in_range), 0)) {
-        double s2 = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s2 += static_cast<double>(x[e]) * x[e];
-        s2 = over_lanes<L>(s2, [](double p, double q) { return p + q; });
-        s2 = inv_sqrt(s2 * (1.0 / D) + static_cast<double>(eps));
-        if (!in_range) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(x[e] * s2);
-          s = 1.f;
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      x[e] = x[e] * s * static_cast<T>(bf16_to_f32(static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)))));
-  }
-  if (rot == 0) return;
-  if (adjacent) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 2)
-      if (li * 8 + e < rot) {
-        const int i = li * 4 + e / 2;
-        const T c = cs[2 * i], s = cs[2 * i + 1], a = x[e], b = x[e + 1];
-        x[e] = a * c - b * s;
-        x[e + 1] = b * c + a * s;
-      }
-    return;
-  }
-  // partner dims are rot / 2 = 8 * hl away; lanes past rot read some lane and keep their own
-  const int hl = rot / 16;
-  const int lane = threadIdx.x & 63, base = lane - li;
-  const bool first = li < hl, second = !first && li < 2 * hl;
-  const int partner = base + (first ? li + hl : second ? li - hl : li);
-  if constexpr (L == 16)
-    if (2 * hl == L) {  // all of a head of 128 dims: the partner is 8 lanes away in the same 16
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const T y = lane_pattern<kTurn8>(x[e]);
-        const int i = (li & 7) * 8 + e;
-        const T c = cs[2 * i], s = cs[2 * i + 1];
-        x[e] = first ? x[e] * c - y * s : x[e] * c + y * s;
-      }
-      return;
-    }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const T y = __shfl(x[e], partner);
-    if (first || second) {
-      const int i = (first ? li : li - hl) * 8 + e;
-      const T c = cs[2 * i], s = cs[2 * i + 1];
-      x[e] = first ? x[e] * c - y * s : x[e] * c + y * s;
-    }
-  }
-}
-
-__device__ __forceinline__ u32x4 pack_bf16(const float (&x)[8]) {
-  u32x4 r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = bf16_pair(x[2 * j], x[2 * j + 1]);
-  return r;
-}
 
 // e2m1 code of x / one for 16-bit x and one, or of fp64 x with one = 1: the
 // borders are multiples of `one`, exact in T.  Nearest, ties to the even code.
@@ -154,11 +33,6 @@ __device__ __forceinline__ uint32_t code_of(T x, T one) {
                      (y > static_cast<T>(2.5) * one) + (y >= static_cast<T>(3.5) * one) +
                      (y > static_cast<T>(5.0) * one);
   return c | (x < 0 ? 8u : 0u);
-}
-
-__device__ __forceinline__ void unpack(const u32x4& v, float (&x)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32(static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1))));
 }
 
 // One key head into a 4-bit page, fp64 throughout: lane li holds 8 of the 32
@@ -451,6 +325,9 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadArgs a) {
         if (j >= first && j < first + n) {
           if constexpr (FMT == DSPARK_CACHE_BF16) {
             x[j] = *reinterpret_cast<const u32x4*>(head + PL::k(a.P, t8 + j, li));
+          } else if constexpr (FMT == DSPARK_CACHE_FP8) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(head + PL::k(a.P, t8 + j, li / 2) + (li & 1) * 8);
+            x[j] = fp8_octet(w[0], w[1], k_scale_value(static_cast<uint8_t>(head[PL::k_scale(a.P, t8)])));
           } else {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(head + PL::k(a.P, t8 + j, li / 4) + (li & 3) * 4);
             x[j] = fp4_octet(w, k_scale_value(static_cast<uint8_t>(head[PL::k_scale(a.P, t8 + j) + li / 4])));
@@ -462,6 +339,9 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadArgs a) {
       for (int e = 0; e < 8; ++e) {
         if constexpr (FMT == DSPARK_CACHE_BF16) {
           y[e] = *reinterpret_cast<const u32x4*>(head + PL::v(a.P, t8, li * 8 + e));
+        } else if constexpr (FMT == DSPARK_CACHE_FP8) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(head + PL::v(a.P, t8, li * 8 + e));
+          y[e] = fp8_octet(w[0], w[1], k_scale_value(static_cast<uint8_t>(head[PL::v_scale(a.P, t8)])));
         } else {
           const u32x4 c = fp4_octet(*reinterpret_cast<const uint32_t*>(head + PL::v(a.P, t8, li * 8 + e)), 1.f);
           const float* sc = reinterpret_cast<const float*>(head + PL::v_scale(a.P, t8));
@@ -528,6 +408,9 @@ hipError_t read_d(int D, ReadArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// cache_append8.hip
+hipError_t cache_append8_launch(int D, AppendArgs& a, hipStream_t s);
+
 hipError_t cache_append_launch(int fmt, int R, int gamma, int Hq, int Hkv, int D, int P, int n_pages, int max_pages,
                                const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
                                const void* wq, const void* wk, float eps, const double* freq, int rot, int adjacent,
@@ -538,7 +421,9 @@ hipError_t cache_append_launch(int fmt, int R, int gamma, int Hq, int Hkv, int D
                ldq, ldk, ldv, static_cast<const uint16_t*>(wq), static_cast<const uint16_t*>(wk), eps, freq, rot,
                adjacent, row0, ell, len, table, static_cast<uint16_t*>(q_out), static_cast<char*>(pool), 0, 0, 0.f,
                0.f, 0.f};
-  return fmt == DSPARK_CACHE_BF16 ? append_d<DSPARK_CACHE_BF16>(D, a, s) : append_d<DSPARK_CACHE_FP4>(D, a, s);
+  return fmt == DSPARK_CACHE_BF16   ? append_d<DSPARK_CACHE_BF16>(D, a, s)
+         : fmt == DSPARK_CACHE_FP8 ? cache_append8_launch(D, a, s)
+                                   : append_d<DSPARK_CACHE_FP4>(D, a, s);
 }
 
 hipError_t cache_read_launch(int fmt, int R, int T, int Hkv, int D, int P, int n_pages, int max_pages,
@@ -546,7 +431,9 @@ hipError_t cache_read_launch(int fmt, int R, int T, int Hkv, int D, int P, int n
                              void* k, void* v, hipStream_t s) {
   ReadArgs a{R, T, Hkv, P, n_pages, max_pages, start, count, table, static_cast<const char*>(pool), 0,
              static_cast<uint16_t*>(k), static_cast<uint16_t*>(v)};
-  return fmt == DSPARK_CACHE_BF16 ? read_d<DSPARK_CACHE_BF16>(D, a, s) : read_d<DSPARK_CACHE_FP4>(D, a, s);
+  return fmt == DSPARK_CACHE_BF16   ? read_d<DSPARK_CACHE_BF16>(D, a, s)
+         : fmt == DSPARK_CACHE_FP8 ? read_d<DSPARK_CACHE_FP8>(D, a, s)
+                                   : read_d<DSPARK_CACHE_FP4>(D, a, s);
 }
 
 }  // namespace dspark

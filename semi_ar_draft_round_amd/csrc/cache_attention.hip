@@ -37,16 +37,13 @@
 // rows are three row tiles, and the fourth wave of the work group idles.
 // Short contexts are bound by the two launches and the chain of loads before
 // the first tile, 6 of 13 us (one token over 1023).
-#include "cache.hpp"
+#include "cache_tiles.hpp"
 
 namespace dspark {
 
 namespace {
 
-constexpr int kTile = 32;       // tokens of a tile, and query rows of a wave
-constexpr int W = 4;            // waves of a work group
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr int W = 4;  // waves of a work group
 
 struct AttnArgs {
   int R, gamma, Hq, Hkv, G, P, n_pages, max_pages;
@@ -78,25 +75,6 @@ struct Desc {
   int wg;
 };
 
-__device__ __forceinline__ bf16x8 as_bf16(u32x4 x) {
-  union {
-    u32x4 u;
-    bf16x8 b;
-  } c;
-  c.u = x;
-  return c.b;
-}
-
-// A (quotient of) counts below 2^52, by a double division and its correction:
-// shorter code than the 64-bit integer division.
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  int64_t q = static_cast<int64_t>(static_cast<double>(x) / static_cast<double>(y));
-  const int64_t r = x - q * y;
-  if (r < 0) --q;
-  if (r >= y) ++q;
-  return q;
-}
-
 // A request's row block: its query rows m0 .. m0 + rows - 1, and the tiles
 // any of them can see: tiles 0 .. head - 1, then first .., count in all.
 // Tokens past the table's reach do not exist, so positions fit 32 bits.
@@ -106,8 +84,6 @@ struct Block {
   int head, first, count;
   int shift;             // log2 of the waves along the rows (1, 2, 4)
 };
-constexpr int kFar = 1 << 29;  // past every table (2^20 pages of 128 tokens)
-
 // Units of a tile by the log2 of the waves along the rows: the time it takes.
 // 16-bit tiles come at the pace of memory until four waves share them; 4-bit
 // ones at that of the vector units nearly from the start.  Measured with heads
@@ -147,93 +123,15 @@ __device__ __forceinline__ Block block_of(const AttnArgs& a, int entry, int rows
 }
 
 // The same in every lane, so in scalar registers.
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ Block uniform(const Block& b) {
+__device__ __forceinline__ Block uniform_block(const Block& b) {
   return Block{uniform(b.m0),   uniform(b.rows),  uniform(b.len),  uniform(b.head),
                uniform(b.first), uniform(b.count), uniform(b.shift)};
 }
 
-// The token that K row slot p (0 .. 15) of a 16-token block holds: with this
-// order the accumulators of half h are tokens 8 h .. 8 h + 7 in turn.
-__device__ __forceinline__ int token_of_slot(int p) { return ((p >> 2) & 1) * 8 + (p >> 3) * 4 + (p & 3); }
-
-// Keeps a rare branch a branch: without it the compiler turns the few
-// instructions inside into selects that every tile pays for.
-__device__ __forceinline__ void rare() { asm volatile(""); }
-
-// Loads before this stay before those after it: they return in the order of
-// their use (the scheduler likes to reverse them, and the first product then
-// waits for the last load).  Everything but vector memory may cross.
-__device__ __forceinline__ void keep_load_order() { __builtin_amdgcn_sched_barrier(0x78F); }
-
-// The operands of one tile, loaded ahead of their use.  K: this lane's row
-// (token slot lane % 32 of the tile), the 8 dims of its half at every step.
-// V: this lane's dim (lane % 32 of every block of 32), the 8 tokens of its
-// half of each 16.  Addresses are a wave's base (the page's part for the head
-// and the token in it, in scalar registers) and a lane's constant offset.
-template <int FMT, int D>
-struct KTile;
+// V of a tile: this lane's dim (lane % 32 of every block of 32), the 8 tokens
+// of its half of each 16.
 template <int FMT, int D>
 struct VTile;
-
-template <int D>
-struct KTile<DSPARK_CACHE_BF16, D> {
-  u32x4 x[D / 16];
-  static __device__ __forceinline__ uint32_t lane_offset(int slot, int h) {
-    return (slot >> 4) * (32 * D) + (h * 16 + token_of_slot(slot & 15)) * 16;
-  }
-  __device__ __forceinline__ void load(const char* head, int, int t, uint32_t lane, int) {
-    const char* p = head + static_cast<int64_t>(t >> 4) * (32 * D);
-#pragma unroll
-    for (int u = 0; u < D / 16; ++u) x[u] = *reinterpret_cast<const u32x4*>(p + u * 512 + lane);
-  }
-  static __device__ __forceinline__ int q_dim(int u, int h) { return 16 * u + 8 * h; }
-  __device__ __forceinline__ f32x16 scores(const u32x4 (&q)[D / 16], int) const {
-    f32x16 s = {0.f};
-#pragma unroll
-    for (int u = 0; u < D / 16; ++u)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(x[u]), as_bf16(q[u]), s, 0, 0, 0);
-    return s;
-  }
-};
-
-// 4 bits: a 16-byte load is 32 dims of a token, one scale group; half h takes
-// groups h, h + 2, ..: four products' operands each, in the order q_dim gives.
-template <int D>
-struct KTile<DSPARK_CACHE_FP4, D> {
-  static constexpr int E = D / 32;
-  u32x4 x[D / 64];
-  uint32_t sc[(E + 3) / 4];
-  static __device__ __forceinline__ uint32_t lane_offset(int slot, int h) {
-    return (slot >> 4) * (8 * D) + (h * 16 + token_of_slot(slot & 15)) * 16;
-  }
-  // token: the lane's token counted from t
-  __device__ __forceinline__ void load(const char* head, int P, int t, uint32_t lane, int token) {
-    const char* p = head + static_cast<int64_t>(t >> 4) * (8 * D);
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g) x[g] = *reinterpret_cast<const u32x4*>(p + g * 512 + lane);
-    const char* b = head + P * (D / 2) + t * E + static_cast<uint32_t>(token * E);
-    if constexpr (E == 2) {
-      sc[0] = *reinterpret_cast<const uint16_t*>(b);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i) sc[i] = *reinterpret_cast<const uint32_t*>(b + 4 * i);
-    }
-  }
-  static __device__ __forceinline__ int q_dim(int u, int h) { return 32 * (2 * (u / 4) + h) + 8 * (u % 4); }
-  __device__ __forceinline__ f32x16 scores(const u32x4 (&q)[D / 16], int h) const {
-    f32x16 s = {0.f};
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g) {
-      const float scale = k_scale_value((sc[g / 2] >> (16 * (g & 1) + 8 * h)) & 0xFFu);
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(fp4_octet(x[g][v], scale)), as_bf16(q[4 * g + v]), s, 0, 0,
-                                                    0);
-    }
-    return s;
-  }
-};
 
 // Weights as two bf16 numbers each: the upper half of the bits, which is not
 // above the weight, and the nearest to what that leaves and 2^-22 of the weight
@@ -322,6 +220,28 @@ struct VTile<DSPARK_CACHE_FP4, D> {
   }
 };
 
+// 8 bits: the scale of a block of 16 tokens goes into its values.
+template <int D>
+struct VTile<DSPARK_CACHE_FP8, D> {
+  static constexpr int E = D / 32;
+  u32x2 x[2][E];
+  float sc[2];
+  static __device__ __forceinline__ uint32_t lane_offset(int row, int h) { return (h * 32 + row) * (8 * E); }
+  __device__ __forceinline__ void load(int s, const char* head, int P, int t, uint32_t lane, int) {
+    const char* p = head + P * D + static_cast<int64_t>(t >> 4) * (16 * D) + lane;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p + 16 * i);
+      x[s][2 * i] = u32x2{w[0], w[1]};
+      x[s][2 * i + 1] = u32x2{w[2], w[3]};
+    }
+    sc[s] = k_scale_value(*reinterpret_cast<const uint8_t*>(head + 2 * P * D + 8 + (t >> 4)));
+  }
+  __device__ __forceinline__ u32x4 operand(int s, int b) const { return fp8_octet(x[s][b][0], x[s][b][1], sc[s]); }
+  __device__ __forceinline__ float weight(int, float p) const { return p; }
+  __device__ __forceinline__ void hide(int, bool) {}
+};
+
 // Running softmax of a lane's query row (m, what weights are relative to, is
 // the row's, l the lane's own tokens') and its part of the output.
 template <int D>
@@ -333,10 +253,10 @@ struct Acc {
 // A visible value that is not finite in a tile that some rows see and others
 // do not: the products above took it as zero, because zero weights times an
 // infinity are NaN; here each row adds what it does see.  Rare and slow.
-template <int D>
+template <int FMT, int D>
 __device__ __forceinline__ void add_non_finite(f32x16 (&o)[D / 32], const float (&p)[16], uint32_t visible,
                                             const char* head0, const char* head1, int P, int t0, int t1, int lane) {
-  typedef PageLayout<DSPARK_CACHE_BF16, D> L;
+  typedef PageLayout<FMT, D> L;
   const int h = lane >> 5;
   for (int t = 0; t < 32; ++t) {
     float w = 0.f;
@@ -358,7 +278,11 @@ __device__ __forceinline__ void add_non_finite(f32x16 (&o)[D / 32], const float 
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int d = b * 32 + 8 * (j / 4) + 4 * h + j % 4;
-        const float v = bf16_to_f32(reinterpret_cast<const uint16_t*>(head + L::v(P, tt, d))[tt & 7]);
+        float v;
+        if constexpr (FMT == DSPARK_CACHE_BF16)
+          v = bf16_to_f32(reinterpret_cast<const uint16_t*>(head + L::v(P, tt, d))[tt & 7]);
+        else
+          v = (head[L::v(P, tt, d) + (tt & 7)] & 0x7F) == 0x7F ? __builtin_nanf("") : 0.f;
         if (see && !(fabsf(v) <= 3.4028234e38f)) o[b][j] += w * v;
       }
   }
@@ -522,7 +446,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   const int per = ceil_div(entries, T);
   const int e0 = min(entries, static_cast<int>(threadIdx.x) * per), e1 = min(entries, e0 + per);
   if (threadIdx.x == 0) lds_run[0] = lds_run[1] = 0;
-  constexpr bool kFavoured = FMT == DSPARK_CACHE_FP4 && D != 256;
+  constexpr bool kFavoured = FMT != DSPARK_CACHE_BF16 && D != 256;
   Deal<kFavoured> deal{0, 0, 0, 0};
   int64_t at = 0, u0 = 0;
   int nb = 0, parts = 0;  // parts of a head; 0: equal runs
@@ -624,7 +548,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 #pragma unroll 1
   for (int64_t u = u0; u < u1;) {
     const int r = entry / a.blocks;
-    const Block b = uniform(block_of(a, entry, rows_max));
+    const Block b = uniform_block(block_of(a, entry, rows_max));
     const int weight = weight_of(FMT, b.shift);
     const int64_t per_head = static_cast<int64_t>(b.count) * weight;
     if (u >= base + per_head * a.Hkv) {
@@ -779,6 +703,33 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
               }
           }
         }
+      } else if constexpr (FMT == DSPARK_CACHE_FP8) {
+        if (!clear) {
+          // the same with codes; a lane none of whose 8 tokens is seen takes no scale either
+          rare();
+#pragma unroll
+          for (int s2 = 0; s2 < 2; ++s2) {
+            u32x2 keep{0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int t = ct + 16 * s2 + 8 * h + e;
+              const bool see = (s2 ? c1 : c0) >= 0 && t <= pos_b && (t >= low_a || t < a.sinks);
+              keep[e / 4] |= see ? 0xFFu << (8 * (e & 3)) : 0u;
+            }
+            vt.sc[s2] = keep[0] | keep[1] ? vt.sc[s2] : 1.f;
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                uint32_t v = vt.x[s2][x][w] & keep[w];
+                // bytes whose lower 7 bits are all ones: adding one to those carries into the top bit
+                const uint32_t nan = ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                odd |= nan != 0u;
+                v &= ~((nan >> 7) * 0xFFu);
+                vt.x[s2][x][w] = v;
+              }
+          }
+        }
       }
 #pragma unroll
       for (int s2 = 0; s2 < 2; ++s2) {
@@ -792,7 +743,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         for (int x = 0; x < NB; x += 2)
           add_weighted(acc.o[x], acc.o[x + 1], vt.operand(s2, x), vt.operand(s2, x + 1), w);
       }
-      if constexpr (FMT == DSPARK_CACHE_BF16)
+      if constexpr (FMT != DSPARK_CACHE_FP4)
         if (__any(odd)) {
           uint32_t visible = 0;
 #pragma unroll
@@ -801,7 +752,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
             const bool see = (j < 8 ? c0 : c1) >= 0 && t <= pos && (t >= low || t < a.sinks);
             visible |= static_cast<uint32_t>(see) << j;
           }
-          add_non_finite<D>(acc.o, p, visible, head_of(c0), head_of(c1), a.P, ct & (a.P - 1), (ct + 16) & (a.P - 1), lane);
+          add_non_finite<FMT, D>(acc.o, p, visible, head_of(c0), head_of(c1), a.P, ct & (a.P - 1), (ct + 16) & (a.P - 1), lane);
         }
     };
 
@@ -886,7 +837,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       // beside this one's exponentials (128 requests x up to 17 rows over
       // ragged contexts up to 16384: 550 -> 511 us with it; 64 x 17 rows, heads
       // of 256 dims, up to 4096: 363 -> 322).
-      constexpr bool kAhead = FMT == DSPARK_CACHE_FP4;
+      constexpr bool kAhead = FMT == DSPARK_CACHE_FP4 || (FMT == DSPARK_CACHE_FP8 && D != 256);
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
       KTile<FMT, D> kt;
@@ -1192,7 +1143,9 @@ hipError_t cache_attention_launch(int fmt, int R, int gamma, int Hq, int Hkv, in
   a.row0 = row0, a.ell = ell, a.len = len, a.table = table;
   a.pool = static_cast<const char*>(pool);
   a.out = static_cast<uint16_t*>(out), a.lse = lse;
-  return fmt == DSPARK_CACHE_BF16 ? run_d<DSPARK_CACHE_BF16>(D, a, ws, s) : run_d<DSPARK_CACHE_FP4>(D, a, ws, s);
+  return fmt == DSPARK_CACHE_BF16 ? run_d<DSPARK_CACHE_BF16>(D, a, ws, s)
+         : fmt == DSPARK_CACHE_FP8 ? run_d<DSPARK_CACHE_FP8>(D, a, ws, s)
+                                   : run_d<DSPARK_CACHE_FP4>(D, a, ws, s);
 }
 
 }  // namespace dspark

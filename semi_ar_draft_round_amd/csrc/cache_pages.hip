@@ -1,4 +1,5 @@
-// Who owns the cache's pages: reserve, commit, fork, compact, copy, reset
+// Who owns the cache's pages: reserve, commit, evict, fork, compact, copy,
+// reset
 // (include/dspark_cache.h).
 //
 // The free pages are a bitmap, so that which ids come next depends on the set
@@ -35,6 +36,11 @@ __device__ int block_exclusive_scan(int v, int* lds, int* total) {
 __device__ __forceinline__ void release(int id, int n_pages, int32_t* ref, uint32_t* bits) {
   if (page_or_none(id, n_pages) < 0) return;
   if (atomicSub(&ref[id], 1) == 1) atomicOr(&bits[id >> 5], 1u << (id & 31));
+}
+
+constexpr int kEvicted = -2;  // table entry of a page that dspark_cache_evict let go
+__device__ __forceinline__ int page_or_mark(int id, int n_pages) {
+  return id == kEvicted ? kEvicted : page_or_none(id, n_pages);
 }
 
 // Bits of word w that stand for pages below n.
@@ -194,8 +200,10 @@ __global__ __launch_bounds__(kT) void cache_reserve_kernel(int R, int gamma, int
   }
 }
 
-// One wave per request.  Pages in use are contiguous in a row (evicted ones
-// lie before them, free entries behind), so both searches end at a -1.
+// One wave per request.  Pages in use are contiguous in a row (released ones
+// lie before them, free entries behind) but for those that dspark_cache_evict
+// let go, which read kEvicted: both searches end at another entry that is no
+// page, and the second one's way is marked -1 as far as it came.
 __global__ __launch_bounds__(256) void cache_commit_kernel(int R, int gamma, int P, int n_pages, int max_pages,
                                                            int window, int sinks, const int32_t* ell,
                                                            const int32_t* n_acc, int32_t* len, int32_t* table,
@@ -224,11 +232,11 @@ __global__ __launch_bounds__(256) void cache_commit_kernel(int R, int gamma, int
   const int64_t keep = (static_cast<int64_t>(sinks) + P - 1) / P;
   for (int64_t i = dead - 1 - lane; ; i -= 64) {
     const int id = i >= keep ? row[i] : -1;
-    if (id >= 0) {
+    if (id >= 0 || id == kEvicted) {
       row[i] = -1;
       release(id, n_pages, ref, bits);
     }
-    if (__ballot(id < 0)) break;
+    if (__ballot(id < 0 && id != kEvicted)) break;
   }
 }
 
@@ -252,7 +260,7 @@ __global__ __launch_bounds__(256) void cache_fork_take(int R, int P, int n_pages
   const int32_t* src = table + static_cast<int64_t>(s) * max_pages;
   int32_t* dst = new_table + static_cast<int64_t>(r) * max_pages;
   for (int i = threadIdx.x; i < max_pages; i += 256) {
-    const int id = i < pages ? page_or_none(src[i], n_pages) : -1;
+    const int id = i < pages ? page_or_mark(src[i], n_pages) : -1;
     dst[i] = id;
     if (id >= 0) atomicAdd(&ref[id], 1);
   }
@@ -295,7 +303,7 @@ __global__ __launch_bounds__(kT) void cache_fork_small(int R, int P, int n_pages
     if (s < 0) continue;
     new_len[j] = len[s];
     const int64_t pages = (static_cast<int64_t>(max(new_len[j], 0)) + P - 1) / P;
-    if (i < pages) id[j] = page_or_none(table[s * max_pages + i], n_pages);
+    if (i < pages) id[j] = page_or_mark(table[s * max_pages + i], n_pages);
   }
 #pragma unroll
   for (int j = 0; j < kForkPer; ++j)
@@ -314,6 +322,120 @@ __global__ __launch_bounds__(kT) void cache_fork_small(int R, int P, int n_pages
       table[e] = id[j];
       if (e % max_pages == 0) len[e / max_pages] = new_len[j];
     }
+}
+
+// Eviction, a work group a request: the k-th smallest mass of the pages that
+// may go is found a byte at a time from the top (four passes over keys, with
+// their counts in LDS), then the pages below it go, and of those equal to it
+// the first by entry.  Keys of up to kEvictPer a thread stay in registers, of
+// longer tables they are made again from memory in every pass.
+constexpr int kEvictPer = 8;
+
+// Smaller mass, smaller key; -0 as 0, NaN above all.
+__device__ __forceinline__ uint32_t mass_key(float m) {
+  return m != m ? 0xFFFFFFFFu : ordered_bits(m + 0.f);
+}
+
+template <bool LONG>
+__global__ __launch_bounds__(kT) void cache_evict_kernel(int R, int P, int n_pages, int max_pages, int sinks,
+                                                         int recent, const int32_t* budget, const int32_t* len,
+                                                         float* mass, int32_t* table, int32_t* ref, uint32_t* bits,
+                                                         int32_t* freed) {
+  __shared__ int lds[kT / 64];
+  __shared__ int count[256];
+  __shared__ int s_digit, s_left;
+  const int r = blockIdx.x, most = budget[r];
+  const int64_t n = len[r];
+  int32_t* row = table + static_cast<int64_t>(r) * max_pages;
+  float* weight = mass + static_cast<int64_t>(r) * max_pages;
+  const int used = n <= 0 ? 0 : static_cast<int>(min((n + P - 1) / P, static_cast<int64_t>(max_pages)));
+  if (most < 0 || used <= most) {  // the same for all threads
+    if (threadIdx.x == 0 && freed) freed[r] = 0;
+    return;
+  }
+  // entries that may go: first .. end - 1
+  const int first = static_cast<int>(min((static_cast<int64_t>(sinks) + P - 1) / P, static_cast<int64_t>(used)));
+  const int end = n > recent ? static_cast<int>(min((n - recent) / P, static_cast<int64_t>(used))) : 0;
+  const int rounds = ceil_div(used, kT);
+  bool may[kEvictPer];
+  uint32_t key[kEvictPer];
+  int held = 0, able = 0;
+  auto look = [&](int i, bool& can, uint32_t& k) {
+    const int s = i * kT + threadIdx.x;
+    const bool have = s < used && page_or_none(row[s], n_pages) >= 0;
+    can = have && s >= first && s < end;
+    k = can ? mass_key(weight[s]) : 0u;
+    return have;
+  };
+  if constexpr (LONG) {
+    for (int i = 0; i < rounds; ++i) {
+      held += look(i, may[0], key[0]);
+      able += may[0];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) {
+      held += look(i, may[i], key[i]);
+      able += may[i];
+    }
+  }
+  block_exclusive_scan(held, lds, &held);
+  block_exclusive_scan(able, lds, &able);
+  const int k = min(held - most, able);
+  if (threadIdx.x == 0 && freed) freed[r] = max(k, 0);
+  if (k <= 0) return;
+  // every key below `prefix` goes, and `left` of those that equal it
+  uint32_t prefix = 0;
+  int left = k;
+#pragma unroll 1
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (threadIdx.x < 256) count[threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t above = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    auto tally = [&](bool can, uint32_t x) {
+      if (can && (x & above) == prefix) atomicAdd(&count[(x >> shift) & 255], 1);
+    };
+    if constexpr (LONG) {
+      for (int i = 0; i < rounds; ++i) {
+        look(i, may[0], key[0]);
+        tally(may[0], key[0]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEvictPer; ++i) tally(may[i], key[i]);
+    }
+    __syncthreads();
+    const int c = threadIdx.x < 256 ? count[threadIdx.x] : 0;
+    int all;
+    const int before = block_exclusive_scan(c, lds, &all);
+    if (before < left && left <= before + c) s_digit = threadIdx.x, s_left = left - before;
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(s_digit) << shift;
+    left = s_left;
+    __syncthreads();
+  }
+  int equal_before = 0;  // keys equal to prefix in the rounds so far
+  auto drop = [&](int i, bool can, uint32_t x) {
+    const bool tie = can && x == prefix;
+    int ties;
+    const int at = equal_before + block_exclusive_scan(tie, lds, &ties);
+    equal_before += ties;
+    if ((can && x < prefix) || (tie && at < left)) {
+      const int s = i * kT + threadIdx.x;
+      release(row[s], n_pages, ref, bits);
+      row[s] = kEvicted;
+      weight[s] = 0.f;
+    }
+  };
+  if constexpr (LONG) {
+    for (int i = 0; i < rounds; ++i) {
+      look(i, may[0], key[0]);
+      drop(i, may[0], key[0]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) drop(i, may[i], key[i]);
+  }
 }
 
 // ws: word 0 = U, then the new id of every page that moves.
@@ -423,6 +545,18 @@ hipError_t cache_commit_launch(int R, int gamma, int P, int n_pages, int max_pag
                                uint32_t* bits, hipStream_t s) {
   cache_commit_kernel<<<ceil_div(R, 4), 256, 0, s>>>(R, gamma, P, n_pages, max_pages, window, sinks, ell, n_acc, len,
                                                      table, ref, bits);
+  return hipGetLastError();
+}
+
+hipError_t cache_evict_launch(int R, int P, int n_pages, int max_pages, int sinks, int recent, const int32_t* budget,
+                              const int32_t* len, float* mass, int32_t* table, int32_t* ref, uint32_t* bits,
+                              int32_t* freed, hipStream_t s) {
+  if (max_pages <= kEvictPer * kT)
+    cache_evict_kernel<false><<<R, kT, 0, s>>>(R, P, n_pages, max_pages, sinks, recent, budget, len, mass, table, ref,
+                                               bits, freed);
+  else
+    cache_evict_kernel<true><<<R, kT, 0, s>>>(R, P, n_pages, max_pages, sinks, recent, budget, len, mass, table, ref,
+                                              bits, freed);
   return hipGetLastError();
 }
 

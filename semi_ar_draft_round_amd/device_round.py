@@ -215,22 +215,31 @@ def run_round_four_calls(d: DeviceRound):
     verify(d)
 
 
-def run_round_cached(d: DeviceRound, cache, forward):
+def run_round_cached(d: DeviceRound, cache, forward, conditions=None, mask=None):
     """The round with the target's paged cache (cache.PagedCache) in it:
     pages for the admitted rows after the schedule, forward(d, cache, ell) as
     the target's pass over them (cache.append and cache.attend per layer; its
     logits go to d.target), and after the verification the accepted rows
     kept.  A request that got no pages (ell -1) keeps its cache as it was and
     has to draft from the same anchor again: its next_tok is its x0, and its
-    n_acc is -1."""
+    n_acc is -1.  With `conditions` (logits.Conditions) the target's logits get
+    every request's penalties and biases, and `mask` ([R (gamma + 1)][ceil(V /
+    32)], what a grammar allows after each draft), before they are verified
+    against; what is kept joins the history."""
+    if mask is not None and conditions is None:
+        raise ValueError("a mask needs conditions")
     sample_conf(d)
     schedule(d)
     ell = cache.reserve(d.ell, d.gamma)
     forward(d, cache, ell)
+    if conditions is not None:
+        conditions.apply(d.target, ell, d.gamma, d.x0, d.x, mask=mask)
     verify(d, ell)
     refused = ell < 0
     torch.where(refused, d.x0, d.next_tok, out=d.next_tok)
     d.n_acc.masked_fill_(refused, -1)
+    if conditions is not None:
+        conditions.commit(ell, d.n_acc, d.x0, d.x)
     cache.commit(d.n_acc)
 
 
