@@ -40,7 +40,8 @@ extern "C" {
  *   l <- l + bias
  *   l <- -inf                                           if v is not allowed
  * in fp32, rounded once to dt.  Rows of nobody are left as they were.  A row
- * that allows nothing is -inf throughout.
+ * that allows nothing is -inf throughout (dspark_verify then accepts no draft
+ * there, and what it draws is any token).
  *
  *   logits   [rows][V] dt;  out [rows][V] dt out (may be logits)
  *   state    [R][V] u16 or NULL (no history: x0 and x are not counted either)

@@ -918,6 +918,8 @@ def dspark_logits(logits, state, ell, gamma, x0, x=None, *, row0=None, repetitio
     per = [None if t is None else _need(t, n, (R,), torch.float32, dev)
            for t, n in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency"))]
     nb, p_tok, p_bias = 0, None, None
+    if (bias_tok is None) != (bias is None):
+        raise ValueError("bias_tok and bias come together")
     if bias_tok is not None:
         nb = bias_tok.shape[-1]
         p_tok = _need(bias_tok, "bias_tok", (R, nb), _I32, dev)
