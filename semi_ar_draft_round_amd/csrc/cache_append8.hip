@@ -1,16 +1,18 @@
 // The append into 8-bit pages: norms and rotation as for the other formats,
 // and blocks of 16 tokens that share a scale (include/dspark_cache.h).
 //
-// A block's scale is known when all of its new rows are, so one wave takes a
-// block's keys of one head, another its values: it holds the block's new rows
-// in registers, finds their largest magnitude, compares the scale that the
-// block's committed tokens have, and writes codes.  Only where the scale grew
-// are the committed tokens' codes read, rounded again and written back.
-//   keys    D / 8 lanes a row, 8 dims each, as the norm and the rotation want
-//           it; fp64, so that a code does not depend on the order of a sum;
-//   values  a lane has its dims of all 16 tokens, which is how the pages hold
-//           them: no exchange, whole 8-byte words.
-// Queries go to work groups of their own, as a head slot a row and head.
+// A block's scale is known when all of its new rows are, so a task is a
+// block's keys of some heads, or its values: the rows are held in registers,
+// their largest magnitudes meet in LDS, the scale that the block's committed
+// tokens have is compared, and codes are written.  Only where the scale grew
+// are the committed tokens' codes read, rounded again and written back.  With
+// two threads a dim, whatever D is, a task has 16 slots of D / 8 threads:
+//   keys     a slot for a (head, row): as many heads as have room, so that the
+//            few rows that most requests bring fill the work group; fp64, so
+//            that a code does not depend on the order of a sum;
+//   values   a thread for a dim's 8 tokens, a word of the pages: one head, or
+//            two where the rows touch one half of the block;
+//   queries  a slot for a (row, head).
 //
 // A code is rounded once: fp64 is cut to fp32 with what was cut off kept in
 // the last bit (a value between two codes, or between a code and the border
@@ -23,16 +25,18 @@ namespace {
 
 constexpr int kBlock = 16;  // tokens that share a scale
 constexpr int kLow = -117, kHigh = 119;  // exponents of a scale
-constexpr float kMost = 448.f;           // the largest code
 
-// y cut to fp32, its last bit set if anything was lost; |y| <= 448.
-__device__ __forceinline__ float cut_odd(double y) {
-  const uint64_t b = __double_as_longlong(y);
-  const int ex = static_cast<int>((b >> 52) & 0x7FF) - 1023 + 127;
-  const uint32_t sign = static_cast<uint32_t>(b >> 63) << 31;
-  if (ex <= 0) return __uint_as_float(sign);  // below 2^-126: far below half of the least code
-  const uint32_t m = static_cast<uint32_t>(b >> 29) & 0x7FFFFFu, lost = (b & 0x1FFFFFFFull) != 0;
-  return __uint_as_float(sign | static_cast<uint32_t>(ex) << 23 | m | lost);
+constexpr float kEnd = 448.f * 0x1p119f;  // what larger numbers are held as
+
+// x cut to fp32, its last bit set if anything was lost; past kEnd that, and
+// NaN for what is not finite.
+__device__ __forceinline__ float cut_odd(double x) {
+  const double y = fmin(fmax(x, -static_cast<double>(kEnd)), static_cast<double>(kEnd));
+  const float f = static_cast<float>(y);  // to nearest: at most one step beyond y
+  const double z = static_cast<double>(f);
+  uint32_t b = __float_as_uint(f) - (fabs(z) > fabs(y) ? 1u : 0u);
+  b |= z != y ? 1u : 0u;
+  return fabs(x) <= 1.7976931348623157e308 ? __uint_as_float(b) : __builtin_nanf("");
 }
 
 // Four e4m3 codes, each to nearest, ties to even; |x| <= 448 or NaN.
@@ -47,250 +51,254 @@ __device__ __forceinline__ uint32_t rescale(uint32_t w, float f) {
   return codes_of(a[0] * f, a[1] * f, b[0] * f, b[1] * f);
 }
 
-// The smallest exponent e with x <= 448 2^e, within the limits.
-__device__ __forceinline__ int exponent_for(double x) {
-  if (!(x > 0)) return kLow;
-  const int q = ilogb(x);  // 448 = 1.75 2^8
-  return min(kHigh, max(kLow, ldexp(x, -q) <= 1.75 ? q - 8 : q - 7));
+// The smallest exponent e with x <= 448 2^e = 1.75 2^(e + 8), within the limits; x >= 0.
+__device__ __forceinline__ int exponent_for(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return min(kHigh, max(kLow, static_cast<int>(b >> 23) - 127 - ((b & 0x7FFFFFu) <= 0x600000u ? 8 : 7)));
 }
 __device__ __forceinline__ int exponent_of(uint8_t byte) { return min(kHigh, max(kLow, static_cast<int>(byte) - 127)); }
 
-// 16 tokens of one request's row of blocks: tokens first .. first + n - 1 of
-// the block are new, those before `first` committed.
-struct Block {
-  int first, n;
-  int64_t row;   // of the first new token
-  int64_t t0;    // its position
-  int t;         // the block's first token within its page
-  char* page;
-};
-
-template <int D>
-__device__ __forceinline__ void append_keys(const AppendArgs& a, const Block& b, int head, int lane, const u32x4& w_k,
-                                            const u32x4 (&raw)[kBlock * D / 512], const double* cs) {
-  typedef PageLayout<DSPARK_CACHE_FP8, D> PL;
-  constexpr int L = D / 8, RW = 64 / L, IT = kBlock / RW;
-  const int li = lane % L, sub = lane / L;
-  double x[IT][8], top = 0;
-#pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int j = it * RW + sub;
-    const bool mine = j >= b.first && j < b.first + b.n;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[it][e] = 0;
-    if (it * RW + RW <= b.first || it * RW >= b.first + b.n) continue;  // the same in every lane
-    float f[8];
-    unpack(raw[it], f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[it][e] = f[e];
-    norm_rotate<double, D>(x[it], li, a.wk != nullptr, w_k, a.eps, a.rot, a.adjacent != 0,
-                           cs + (mine ? j - b.first : 0) * D);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (!mine) x[it][e] = 0;
-      if (fabs(x[it][e]) <= 1.7976931348623157e308) top = fmax(top, fabs(x[it][e]));
-    }
-  }
-  if (!b.page) return;
-  top = over_lanes<32>(top, [](double p, double q) { return fmax(p, q); });
-  top = fmax(top, __shfl_xor(top, 32));
-  char* hp = b.page + head * PL::head_bytes(a.P);
-  uint8_t* byte = reinterpret_cast<uint8_t*>(hp + PL::k_scale(a.P, b.t));
-  const int before = b.first > 0 ? exponent_of(*byte) : kLow;
-  const int e2 = max(before, exponent_for(top));
-  const double f = ldexp(1.0, -e2);
-  const float again = ldexpf(1.f, before - e2);
-#pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int j = it * RW + sub;
-    u32x2* p = reinterpret_cast<u32x2*>(hp + PL::k(a.P, b.t + j, li / 2) + (li & 1) * 8);
-    if (j >= b.first && j < b.first + b.n) {
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double v = x[it][e];
-        y[e] = fabs(v) <= 1.7976931348623157e308 ? cut_odd(fmin(fmax(v * f, -448.0), 448.0)) : __builtin_nanf("");
-      }
-      *p = u32x2{codes_of(y[0], y[1], y[2], y[3]), codes_of(y[4], y[5], y[6], y[7])};
-    } else if (j < b.first && e2 > before) {
-      const u32x2 w = *p;
-      *p = u32x2{rescale(w[0], again), rescale(w[1], again)};
-    }
-  }
-  if (lane == 0) *byte = static_cast<uint8_t>(e2 + 127);
+// The largest of a wave's values, in every lane.
+__device__ __forceinline__ float largest(float x) {
+  x = over_lanes<32>(x, [](float p, float q) { return fmaxf(p, q); });
+  return fmaxf(x, xor32(x));
 }
 
+// The grid's x are a request's blocks, its y take a block's tasks in turn:
+// keys, values, queries.
 template <int D>
-__device__ __forceinline__ void append_values(const AppendArgs& a, const Block& b, int head, int lane) {
+__global__ __launch_bounds__(2 * D) void cache_append8_kernel(AppendArgs a) {
   typedef PageLayout<DSPARK_CACHE_FP8, D> PL;
-  constexpr int DP = D / 64;  // dims of a lane
-  if (!b.page) return;
-  char* hp = b.page + head * PL::head_bytes(a.P);
-  uint8_t* byte = reinterpret_cast<uint8_t*>(hp + PL::v_scale(a.P, b.t));
-  const int before = b.first > 0 ? exponent_of(*byte) : kLow;
-  const uint16_t* src = a.v + static_cast<int64_t>(head) * D + lane * DP;
-  float x[DP][kBlock], top = 0.f;
-#pragma unroll
-  for (int j = 0; j < kBlock; ++j) {
-    uint16_t v[DP];
-#pragma unroll
-    for (int d = 0; d < DP; ++d) v[d] = 0;
-    if (j >= b.first && j < b.first + b.n)
-      __builtin_memcpy(v, __builtin_assume_aligned(src + (b.row + j - b.first) * a.ldv, 2 * DP), 2 * DP);
-#pragma unroll
-    for (int d = 0; d < DP; ++d) x[d][j] = bf16_to_f32(v[d]);
-  }
-#pragma unroll
-  for (int d = 0; d < DP; ++d)
-#pragma unroll
-    for (int j = 0; j < kBlock; ++j)
-      if (fabsf(x[d][j]) <= 3.4028234e38f) top = fmaxf(top, fabsf(x[d][j]));
-  top = over_lanes<32>(top, [](float p, float q) { return fmaxf(p, q); });
-  top = fmaxf(top, xor32(top));
-  const int e2 = max(before, exponent_for(top));
-  const float f = ldexpf(1.f, -e2), again = ldexpf(1.f, before - e2);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    // bits of the new tokens, and of the committed ones, among these eight
-    const int lo = min(max(b.first - 8 * h, 0), 8), hi = min(max(b.first + b.n - 8 * h, 0), 8);
-    const uint64_t upto = hi == 8 ? ~0ull : (1ull << (8 * hi)) - 1ull, old = lo == 8 ? ~0ull : (1ull << (8 * lo)) - 1ull;
-    const uint64_t fresh = upto & ~old;
-    const bool grown = old && e2 > before;
-    if (!fresh && !grown) continue;
-#pragma unroll
-    for (int d = 0; d < DP; ++d) {
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = x[d][8 * h + j];
-        y[j] = fabsf(v) <= 3.4028234e38f ? fminf(fmaxf(v * f, -kMost), kMost) : __builtin_nanf("");
-      }
-      u32x2 w{codes_of(y[0], y[1], y[2], y[3]), codes_of(y[4], y[5], y[6], y[7])};
-      u32x2* p = reinterpret_cast<u32x2*>(hp + PL::v(a.P, b.t + 8 * h, lane * DP + d));
-      if (fresh != ~0ull) {
-        const u32x2 was = *p;
-        const u32x2 kept = grown ? u32x2{rescale(was[0], again), rescale(was[1], again)} : was;
-        const uint32_t n0 = static_cast<uint32_t>(fresh), n1 = static_cast<uint32_t>(fresh >> 32);
-        const uint32_t o0 = static_cast<uint32_t>(old), o1 = static_cast<uint32_t>(old >> 32);
-        w[0] = (w[0] & n0) | (kept[0] & o0) | (was[0] & ~(n0 | o0));
-        w[1] = (w[1] & n1) | (kept[1] & o1) | (was[1] & ~(n1 | o1));
-      }
-      *p = w;
-    }
-  }
-  if (lane == 0) *byte = static_cast<uint8_t>(e2 + 127);
-}
-
-// Work groups of a block: `parts` of keys and as many of values, four heads
-// each, then those of queries.
-template <int D>
-__global__ __launch_bounds__(kThreads) void cache_append8_kernel(AppendArgs a, int parts) {
-  constexpr int L = D / 8, kHeads = kThreads / L;
-  __shared__ double lds[kBlock * D];
-  const int r = blockIdx.z, y = blockIdx.y;
+  constexpr int T = 2 * D, L = D / 8;
+  static_assert(T / L == kBlock, "a token or a head for every L threads");
+  __shared__ double cs64[kBlock * D];  // cosines and sines of the new rows: for keys,
+  __shared__ float cs[kBlock * D];     // and for queries
+  __shared__ uint32_t tops[3][kBlock];
+  const int r = blockIdx.z;
   const int half = a.rot / 2;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, li = threadIdx.x % L;
+  const int slot = threadIdx.x / L, li = threadIdx.x % L;
   // what does not depend on anything, at once
   const int n_rows = rows_of(a.ell[r], a.gamma);
   const int64_t len = a.len[r];
   const int64_t row0 = a.row0 ? static_cast<int64_t>(a.row0[r]) : static_cast<int64_t>(r) * (a.gamma + 1);
-  const int pair0 = threadIdx.x - small_quotient(threadIdx.x, a.per_half) * half;
-  const double freq0 = half ? a.freq[pair0] : 0.0;
-  u32x4 w{0u, 0u, 0u, 0u};
-  const uint16_t* norm = y < parts ? a.wk : a.wq;
-  if (norm) w = *reinterpret_cast<const u32x4*>(norm + li * 8);
+  const int part = small_quotient(threadIdx.x, a.per_half), pair = threadIdx.x - part * half;
+  const double freq = half ? a.freq[pair] : 0.0;
+  u32x4 w_q{0u, 0u, 0u, 0u}, w_k{0u, 0u, 0u, 0u};
+  if (a.wq) w_q = *reinterpret_cast<const u32x4*>(a.wq + li * 8);
+  if (a.wk) w_k = *reinterpret_cast<const u32x4*>(a.wk + li * 8);
   if (len < 0) return;
+  // tokens first .. first + n - 1 of the block are new, those before committed
   const int64_t base = (len / kBlock + blockIdx.x) * kBlock;
   const int64_t t0 = base > len ? base : len;
   const int64_t t1 = base + kBlock < len + n_rows ? base + kBlock : len + n_rows;
   if (t0 >= t1) return;
-  const int64_t slot = base >> a.page_shift;
-  const int id = slot < a.max_pages ? page_or_none(a.table[static_cast<int64_t>(r) * a.max_pages + slot], a.n_pages)
-                                    : -1;
-  const Block b{static_cast<int>(t0 - base), static_cast<int>(t1 - t0), row0 + (t0 - len), t0,
-                static_cast<int>(base & (a.P - 1)), id >= 0 ? a.pool + id * a.page_bytes : nullptr};
-  auto turns_of = [&](int row, int p, int i) {
-    const double f = i == static_cast<int>(threadIdx.x) || kThreads % half == 0 ? freq0 : a.freq[p];
-    const double turns = static_cast<double>(t0 + row) * f * 0.15915494309189535;
-    return turns - rint(turns);
-  };
+  const int first = static_cast<int>(t0 - base), n = static_cast<int>(t1 - t0);
+  const int64_t row = row0 + (t0 - len);
+  const float per_n = 1.f / n;
+  const int h0 = first >> 3, both = (first + n - 1) >> 3 != h0;  // the block's halves that the rows touch
+  const int heads_k = small_quotient(kBlock, per_n), heads_v = both ? 1 : 2;
+  const int end_k = ceil_div(a.Hkv, heads_k), end_v = end_k + ceil_div(a.Hkv, heads_v);
+  const int nq = n * a.Hq, tasks = end_v + ceil_div(nq, kBlock);
+  const int step = gridDim.y;
+  int task = blockIdx.y;
+  if (task >= tasks) return;
+  const int64_t place = base >> a.page_shift;
+  const int id = place < a.max_pages ? page_or_none(a.table[static_cast<int64_t>(r) * a.max_pages + place], a.n_pages)
+                                     : -1;
+  char* const page = id >= 0 ? a.pool + id * a.page_bytes : nullptr;
+  const int t = static_cast<int>(base & (a.P - 1));
 
-  if (y < parts) {
-    constexpr int RW = 64 / L, IT = kBlock / RW;
-    const int head = min(4 * y + wave, a.Hkv - 1);
-    u32x4 raw[IT];
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int j = it * RW + lane / L;
-      raw[it] = u32x4{0u, 0u, 0u, 0u};
-      if (j >= b.first && j < b.first + b.n)
-        raw[it] = *reinterpret_cast<const u32x4*>(a.k + (b.row + j - b.first) * a.ldk + static_cast<int64_t>(head) * D + li * 8);
-    }
-    for (int i = threadIdx.x; i < b.n * half; i += kThreads) {
-      const int row = small_quotient(i, a.per_half), p = i - row * half;
-      double s, c;
-      sincospi(2.0 * turns_of(row, p, i), &s, &c);
-      lds[row * D + 2 * p] = c;
-      lds[row * D + 2 * p + 1] = s;
-    }
-    __syncthreads();
-    if (4 * y + wave < a.Hkv) append_keys<D>(a, b, head, lane, w, raw, lds);
-    return;
-  }
-  if (y < 2 * parts) {
-    const int head = 4 * (y - parts) + wave;
-    if (head < a.Hkv) append_values<D>(a, b, head, lane);
-    return;
-  }
-  // queries: a contiguous run of heads of rows, whole rounds of head slots
-  const int nq = b.n * a.Hq;
-  const int rounds = ceil_div(nq, kHeads * static_cast<int>(gridDim.y - 2 * parts));
-  const int u_lo = (y - 2 * parts) * rounds * kHeads, u_hi = min(nq, u_lo + rounds * kHeads);
-  if (u_lo >= u_hi) return;
-  float* cs = reinterpret_cast<float*>(lds);
-  auto source = [&](int u) {
-    const int j = small_quotient(u, a.per_q);
-    return a.q + (b.row + j) * a.ldq + (u - j * a.Hq) * D + li * 8;
+  // this slot's (head, row) of a task of keys
+  const int hk = small_quotient(slot, per_n), jk = slot - hk * n;
+  auto load_k = [&](int task) {
+    const int head = task * heads_k + hk;
+    return hk < heads_k && head < a.Hkv
+               ? *reinterpret_cast<const u32x4*>(a.k + (row + jk) * a.ldk + static_cast<int64_t>(head) * D + li * 8)
+               : u32x4{0u, 0u, 0u, 0u};
   };
-  int u = u_lo + threadIdx.x / L;
-  u32x4 raw{0u, 0u, 0u, 0u};
-  if (u < u_hi) raw = *reinterpret_cast<const u32x4*>(source(u));
-  const int j_a = small_quotient(u_lo, a.per_q), j_b = small_quotient(u_hi - 1, a.per_q);
-  for (int i = threadIdx.x; i < (j_b - j_a + 1) * half; i += kThreads) {
-    const int j = small_quotient(i, a.per_half), p = i - j * half, row = j_a + j;
-    float s, c;
-    sincospif(2.f * static_cast<float>(turns_of(row, p, i)), &s, &c);
-    cs[row * D + 2 * p] = c;
-    cs[row * D + 2 * p + 1] = s;
+  auto load_q = [&](int task) {
+    const int u = (task - end_v) * kBlock + slot, i = small_quotient(u, a.per_q);
+    return u >= 0 && u < nq ? *reinterpret_cast<const u32x4*>(a.q + (row + i) * a.ldq + (u - i * a.Hq) * D + li * 8)
+                            : u32x4{0u, 0u, 0u, 0u};
+  };
+  const bool keys = task < end_k;
+  u32x4 raw = keys ? load_k(task) : load_q(task);
+
+  // sines and cosines of the block's new rows, a run of rows of a pair a
+  // thread: in fp32 for queries; for keys in fp64, the run's first and the
+  // step from row to row, which takes a product where another sine would be
+  if (threadIdx.x < 3 * kBlock) tops[0][threadIdx.x] = 0;
+  if (half) {
+    const int across = T / half;
+    auto turns_of = [&](int i) {
+      const double turns = static_cast<double>(t0 + i) * freq * 0.15915494309189535;
+      return turns - rint(turns);
+    };
+    if (keys) {
+      const int each = ceil_div(n, across), from = part * each, to = part < across ? min(from + each, n) : 0;
+      if (from < to) {
+        const double turn1 = freq * 0.15915494309189535;
+        double c0 = 1, s0 = 0, c1 = 1, s1 = 0;
+#pragma unroll 1
+        for (int k = 0; k < (each > 1 ? 2 : 1); ++k) {
+          c1 = c0, s1 = s0;
+          sincospi(2.0 * (k == 0 && each > 1 ? turn1 - rint(turn1) : turns_of(from)), &s0, &c0);
+        }
+#pragma unroll 1
+        for (int i = from; i < to; ++i) {
+          cs64[i * D + 2 * pair] = c0;
+          cs64[i * D + 2 * pair + 1] = s0;
+          const double c = c0 * c1 - s0 * s1;
+          s0 = s0 * c1 + c0 * s1;
+          c0 = c;
+        }
+      }
+    }
+    {
+#pragma unroll 1
+      for (int i = part; i < n && part < across; i += across) {
+        float s, c;
+        sincospif(2.f * static_cast<float>(turns_of(i)), &s, &c);
+        cs[i * D + 2 * pair] = c;
+        cs[i * D + 2 * pair + 1] = s;
+      }
+    }
   }
   __syncthreads();
+
+  // The exponent of a block's scale, from one thread's contribution of each
+  // slot or wave; the barrier also stands between the loads of the old byte and
+  // its new value.  Of three sets of maxima one is in use, one may still be
+  // read from the task before, and one is cleared for the next.
+  int turn = 0;
+  auto exponent_of_block = [&](float top, bool mine, int which, int before) {
+    if (mine) atomicMax(&tops[turn][which], __float_as_uint(top));
+    const int next = turn == 2 ? 0 : turn + 1;
+    if (threadIdx.x < kBlock) tops[next][threadIdx.x] = 0;
+    __syncthreads();
+    top = __uint_as_float(tops[turn][which]);
+    turn = next;
+    return max(before, exponent_for(top));
+  };
+
 #pragma unroll 1
-  for (; u < u_hi; u += kHeads) {
+  for (; task < end_k; task += step) {
     const u32x4 now = raw;
-    if (u + kHeads < u_hi) raw = *reinterpret_cast<const u32x4*>(source(u + kHeads));
-    const int j = small_quotient(u, a.per_q);
+    raw = task + step < end_k ? load_k(task + step) : load_q(task + step);
+    if (!page) continue;
+    const int head = task * heads_k + hk;
+    const bool live = hk < heads_k && head < a.Hkv;
+    char* hp = page + min(head, a.Hkv - 1) * PL::head_bytes(a.P);
+    uint8_t* byte = reinterpret_cast<uint8_t*>(hp + PL::k_scale(a.P, t));
+    const int before = first > 0 ? exponent_of(*byte) : kLow;
+    float f[8], x[8], top = 0.f;
+    unpack(now, f);
+    double y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = f[e];
+    norm_rotate<double, D>(y, li, a.wk != nullptr, w_k, a.eps, a.rot, a.adjacent != 0, cs64 + jk * D);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = cut_odd(y[e]);
+      top = fmaxf(top, fabsf(x[e]));  // (not a NaN)
+    }
+    top = over_lanes<L>(top, [](float p, float q) { return fmaxf(p, q); });
+    const int e2 = exponent_of_block(top, live && li == 0, min(hk, kBlock - 1), before);
+    if (live) {
+      const float g = ldexpf(1.f, -e2);
+      const int64_t at = (li & 1) * 8;
+      *reinterpret_cast<u32x2*>(hp + PL::k(a.P, t + first + jk, li / 2) + at) =
+          u32x2{codes_of(x[0] * g, x[1] * g, x[2] * g, x[3] * g), codes_of(x[4] * g, x[5] * g, x[6] * g, x[7] * g)};
+      if (e2 > before) {  // the head's slots share its committed tokens
+        const float again = ldexpf(1.f, before - e2);
+        for (int j = jk; j < first; j += n) {
+          u32x2* p = reinterpret_cast<u32x2*>(hp + PL::k(a.P, t + j, li / 2) + at);
+          const u32x2 was = *p;
+          *p = u32x2{rescale(was[0], again), rescale(was[1], again)};
+        }
+      }
+      if (jk == 0 && li == 0) *byte = static_cast<uint8_t>(e2 + 127);
+    }
+  }
+
+#pragma unroll 1
+  for (; task < end_v; task += step) {
+    if (task + step >= end_v) raw = load_q(task + step);
+    if (!page) continue;
+    const int g = threadIdx.x / D, d = threadIdx.x % D;
+    const int head = (task - end_k) * heads_v + (both ? 0 : g), h = both ? g : h0;
+    const bool live = head < a.Hkv;
+    // this thread's tokens are 8 h .. of the block: lo of them committed, up to hi new
+    const int lo = max(first - 8 * h, 0), hi = min(first + n - 8 * h, 8);
+    char* hp = page + min(head, a.Hkv - 1) * PL::head_bytes(a.P);
+    uint8_t* byte = reinterpret_cast<uint8_t*>(hp + PL::v_scale(a.P, t));
+    u32x2* p = reinterpret_cast<u32x2*>(hp + PL::v(a.P, t + 8 * h, d));
+    const int before = first > 0 ? exponent_of(*byte) : kLow;
+    const u32x2 was = *p;
+    const uint16_t* src = a.v + (row + 8 * h - first) * a.ldv + static_cast<int64_t>(min(head, a.Hkv - 1)) * D + d;
+    uint16_t raw_v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) raw_v[j] = src[min(max(j, lo), hi - 1) * a.ldv];  // (all at once: no branches)
+    float x[8], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = j >= lo && j < hi ? bf16_to_f32(raw_v[j]) : 0.f;
+      x[j] = fabsf(v) <= 3.4028234e38f ? fminf(fmaxf(v, -kEnd), kEnd) : __builtin_nanf("");
+      top = fmaxf(top, fabsf(x[j]));  // (not a NaN)
+    }
+    const int e2 = exponent_of_block(largest(top), live && (threadIdx.x & 63) == 0, both ? 0 : g, before);
+    if (live) {
+      const float f = ldexpf(1.f, -e2);
+      u32x2 w{codes_of(x[0] * f, x[1] * f, x[2] * f, x[3] * f), codes_of(x[4] * f, x[5] * f, x[6] * f, x[7] * f)};
+      if (hi - lo < 8) {  // the others' bytes of the word
+        const float again = ldexpf(1.f, before - e2);
+        u32x2 kept = was;
+        if (lo > 0 && e2 > before) kept = u32x2{rescale(was[0], again), rescale(was[1], again)};
+        const uint64_t old = (1ull << (8 * lo)) - 1ull, fresh = (hi == 8 ? ~0ull : (1ull << (8 * hi)) - 1ull) & ~old;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t nw = static_cast<uint32_t>(fresh >> (32 * i)), ow = static_cast<uint32_t>(old >> (32 * i));
+          w[i] = (w[i] & nw) | (kept[i] & ow) | (was[i] & ~(nw | ow));
+        }
+      }
+      if (h0 == 1 && e2 > before) {  // the first half, all of it committed
+        const float again = ldexpf(1.f, before - e2);
+        u32x2* q = reinterpret_cast<u32x2*>(hp + PL::v(a.P, t, d));
+        const u32x2 then = *q;
+        *q = u32x2{rescale(then[0], again), rescale(then[1], again)};
+      }
+      *p = w;
+      if (d == 0 && h == h0) *byte = static_cast<uint8_t>(e2 + 127);
+    }
+  }
+
+#pragma unroll 1
+  for (; task < tasks; task += step) {
+    const u32x4 now = raw;
+    raw = load_q(task + step);
+    const int u = (task - end_v) * kBlock + slot, i = min(small_quotient(u, a.per_q), n - 1);
     float x[8];
     unpack(now, x);
-    norm_rotate<float, D>(x, li, a.wq != nullptr, w, a.eps, a.rot, a.adjacent != 0, cs + j * D);
-    *reinterpret_cast<u32x4*>(a.q_out + ((b.row + j) * a.Hq + (u - j * a.Hq)) * D + li * 8) = pack_bf16(x);
+    norm_rotate<float, D>(x, li, a.wq != nullptr, w_q, a.eps, a.rot, a.adjacent != 0, cs + i * D);
+    if (u < nq) *reinterpret_cast<u32x4*>(a.q_out + ((row + i) * a.Hq + (u - i * a.Hq)) * D + li * 8) = pack_bf16(x);
   }
 }
 
+// Work groups of a compute unit that are asked for.
+constexpr int64_t kPerUnit = 6;
+
 template <int D>
 hipError_t run(AppendArgs& a, hipStream_t s) {
-  constexpr int kHeads = kThreads / (D / 8);
   a.page_bytes = a.Hkv * PageLayout<DSPARK_CACHE_FP8, D>::head_bytes(a.P);
   a.groups = ceil_div(a.gamma + kBlock, kBlock);  // aligned blocks that gamma + 1 tokens can touch
-  const int64_t gx = static_cast<int64_t>(a.R) * a.groups;
-  const int most = ceil_div(kBlock * a.Hq, kHeads);
-  const int64_t want = 12LL * compute_units() / gx;
-  const int gq = want < 1 ? 1 : want > most ? most : static_cast<int>(want);
-  const int parts = ceil_div(a.Hkv, 4);
+  const int64_t want = kPerUnit * compute_units() / (static_cast<int64_t>(a.R) * a.groups);
+  const int rows = a.gamma + 1 < kBlock ? a.gamma + 1 : kBlock;
+  const int most = 2 * a.Hkv + ceil_div(rows * a.Hq, kBlock);
+  const int gy = want < 1 ? 1 : want > most ? most : static_cast<int>(want);
   a.page_shift = __builtin_ctz(a.P);
   a.per_q = 1.f / a.Hq;
-  a.per_k = 1.f / a.Hkv;
   a.per_half = a.rot > 0 ? 2.f / a.rot : 0.f;
-  cache_append8_kernel<D><<<dim3(a.groups, 2 * parts + gq, a.R), kThreads, 0, s>>>(a, parts);
+  cache_append8_kernel<D><<<dim3(a.groups, gy, a.R), 2 * D, 0, s>>>(a);
   return hipGetLastError();
 }
 

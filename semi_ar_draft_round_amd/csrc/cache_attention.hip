@@ -836,8 +836,10 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       // tiles leave room for the next one's scores, whose products then run
       // beside this one's exponentials (128 requests x up to 17 rows over
       // ragged contexts up to 16384: 550 -> 511 us with it; 64 x 17 rows, heads
-      // of 256 dims, up to 4096: 363 -> 322).
-      constexpr bool kAhead = FMT == DSPARK_CACHE_FP4 || (FMT == DSPARK_CACHE_FP8 && D != 256);
+      // of 256 dims, up to 4096: 363 -> 322).  8-bit tiles come at the pace of
+      // memory, and the registers that this takes cost them (32 tokens over
+      // 16384 tokens 152 us with it, 136 without; the 128 requests 617 and 606).
+      constexpr bool kAhead = FMT == DSPARK_CACHE_FP4;
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
       KTile<FMT, D> kt;
