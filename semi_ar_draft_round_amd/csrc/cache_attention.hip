@@ -379,11 +379,16 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   // again once a score passes it: weights are at most 1, so that sums stay as
   // far from overflow as those of a plain softmax, and few tiles rescale.
   constexpr float kSlack = 8.f;
-  constexpr bool kShared = FMT == DSPARK_CACHE_BF16;
+  constexpr bool kShared = FMT == DSPARK_CACHE_BF16 || (FMT == DSPARK_CACHE_FP8 && D == 256);
   // the waves' outputs, on their way to be joined; before that the ring of 16-bit tiles
   __shared__ f32x4 lds_own[W][NB * 4][64];
   __shared__ float2 lds_ml[W][64];
   static_assert((NB * 4) % W == 0, "waves share an output's pieces");
+  // the ring's tiles: of 8 bits twice as many, their pages' scales beside them
+  constexpr bool kBytes = FMT == DSPARK_CACHE_FP8;
+  constexpr int kOps = kBytes ? D / 32 : KS;      // 1 KB operands of a tile's keys, as many of its values
+  constexpr int kRing = kBytes ? 2 * W : W;       // tiles
+  __shared__ u32x4 lds_scale[kShared && kBytes ? kRing : 1][64];
   __shared__ int64_t lds_scan[W];
   __shared__ int64_t lds_base, lds_run[2];
   __shared__ int2 lds_heads[W];
@@ -758,20 +763,22 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
 
     const bool shared = kShared && (D == 256 || b.shift > 0);
     if constexpr (kShared) if (shared) {
-      // Rounds of WT tiles through a ring of W tiles in LDS.  A wave copies
+      // Rounds of WT tiles through a ring of kRing tiles in LDS.  A wave copies
       // its share of every round, whole 1 KB operands in the order the lanes
       // read them, and multiplies its own tile of it.  Copies are issued
-      // W / WT - 1 rounds ahead, past the run's end too (its last tile
+      // kRing / WT - 1 rounds ahead, past the run's end too (its last tile
       // again), so that what is outstanding is known.
-      constexpr int F = D / 8;  // operands of a tile: D / 16 of K, as many of V
-      static_assert(sizeof(lds_own) == W * F * 1024, "the ring lies under the outputs");
+      constexpr int F = 2 * kOps;  // operands of a tile
+      static_assert(sizeof(lds_own) == kRing * F * 1024, "the ring lies under the outputs");
       const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
           (__attribute__((address_space(3))) char*)(&lds_own[0][0][0])));
-      const int depth = W / WT, lw = __ffs(WT) - 1;
+      const uint32_t scale_ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+          (__attribute__((address_space(3))) char*)(&lds_scale[0][0])));
+      constexpr int kBlockBytes = kBytes ? 16 * D : 32 * D;  // of 16 tokens' keys, or values
+      const int depth = kRing / WT, lw = __ffs(WT) - 1;
       const int rounds = (tiles + WT - 1) >> lw;
       const int n = F * WT / W;                   // operands a wave copies in a round
       const int mine = wave * n / F, f0 = wave * n - mine * F;
-      const bool keys = f0 < KS;                  // all of them K, or all V
       Ids from{-1, -1}, own{-1, -1};
       unsigned long long clear_v = 0;
       auto copy = [&](int round) {
@@ -784,19 +791,34 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
         const char* p1 = TWO ? head_of(__builtin_amdgcn_readlane(from.v1, round & 63)) : p0;
         const int t = TWO ? 0 : (tok & (a.P - 1)) >> 4;
         uint32_t to = ring + ((((round & (depth - 1)) << lw) + mine) * F + f0) * 1024;
-        if (keys) {
-          const char* p = (TWO && col >= 16 ? p1 : p0) + t * (32 * D) + f0 * 512 + k_lane;
+        auto copy_k = [&](int n) {
+          const char* p = (TWO && col >= 16 ? p1 : p0) + t * kBlockBytes + f0 * 512 + k_lane;
 #pragma unroll 1
           for (int j = 0; j < n; ++j) copy_to_lds(p + j * 512, to + j * 1024);
-        } else {
-          const int g = f0 - KS;
-          const int64_t v0 = 2 * a.P * D + t * (32 * D) + v_lane;
+        };
+        // operands g .. of V: of 16 bits a 512-byte row of a block for every 32
+        // dims; of 8 bits a lane's words of all of them lie side by side
+        auto copy_v = [&](int g, int n) {
+          constexpr int kHalf = kOps / 2;  // operands of 16 tokens
+          const int64_t v0 = static_cast<int64_t>(kBytes ? 1 : 2) * a.P * D + t * kBlockBytes + v_lane;
 #pragma unroll 1
           for (int j = g; j < g + n; ++j) {
-            const int s2 = j / NB;
-            copy_to_lds((TWO && s2 ? p1 : p0 + (TWO ? 0 : s2 * (32 * D))) + v0 + (j - s2 * NB) * 512, to);
+            const int s2 = j / kHalf;
+            copy_to_lds((TWO && s2 ? p1 : p0 + (TWO ? 0 : s2 * kBlockBytes)) + v0 + (j - s2 * kHalf) * (kBytes ? 16 : 512), to);
             to += 1024;
           }
+        };
+        if constexpr (kBytes) {
+          if (f0 == 0)  // both blocks' scales: 16 bytes of a page, the second one's for the upper half of the lanes
+            copy_to_lds((TWO && h ? p1 : p0) + 2 * a.P * D, scale_ring + (((round & (depth - 1)) << lw) + mine) * 1024);
+          const int n_k = min(max(kOps - f0, 0), n);
+          if (n_k > 0) copy_k(n_k);
+          to += n_k * 1024;
+          if (n_k < n) copy_v(max(f0 - kOps, 0), n - n_k);
+        } else if (f0 < kOps) {
+          copy_k(n);  // (all of them K, or all V)
+        } else {
+          copy_v(f0 - kOps, n);
         }
       };
       for (int round = 0; round < depth - 1; ++round) copy(round);
@@ -804,7 +826,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       for (int round = 0; round < rounds; ++round) {
         // this round's copies are there: those of the depth - 2 after it may be on their way
         if (depth == 2) wait_and_meet<0>();
-        else wait_and_meet<2 * F / W>();
+        else if (!kBytes || depth == 4) wait_and_meet<2 * F / W * (kBytes ? 2 : 1)>();
+        else wait_and_meet<6 * F / W>();
         copy(round + depth - 1);
         if ((round & 63) == 0) {
           rare();
@@ -818,12 +841,24 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
           KTile<FMT, D> kt;
           VTile<FMT, D> vt;
 #pragma unroll
-          for (int u = 0; u < KS; ++u) kt.x[u] = tile[u * 64];
+          for (int u = 0; u < kOps; ++u) kt.x[u] = tile[u * 64];
+          if constexpr (kBytes) {
+            // K scale bytes 0 .. 7 of the page, V's 8 .. 15; block tok >> 4 of the page and the one after it
+            const uint8_t* sc = reinterpret_cast<const uint8_t*>(lds_scale[((round & (depth - 1)) << lw) + wt]);
+            const int b0 = TWO ? 0 : (token_at(t) & (a.P - 1)) >> 4, second = TWO ? 512 : 1;
+            kt.sc = sc[b0 + (col >= 16 ? second : 0)];
+            vt.sc[0] = k_scale_value(sc[8 + b0]);
+            vt.sc[1] = k_scale_value(sc[8 + b0 + second]);
+          }
           const f32x16 s = kt.scores(q, h);
 #pragma unroll
           for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-            for (int x = 0; x < NB; ++x) vt.x[s2][x] = tile[(KS + s2 * NB + x) * 64];
+            for (int x = 0; x < kOps / 2; ++x) {
+              const u32x4 w = tile[(kOps + s2 * (kOps / 2) + x) * 64];
+              if constexpr (kBytes) vt.x[s2][2 * x] = u32x2{w[0], w[1]}, vt.x[s2][2 * x + 1] = u32x2{w[2], w[3]};
+              else vt.x[s2][x] = w;
+            }
           const int c0 = __builtin_amdgcn_readlane(own.v0, round & 63);
           const int c1 = TWO ? __builtin_amdgcn_readlane(own.v1, round & 63) : c0;
           absorb(s, vt, token_at(t), c0, c1, (clear_v >> (round & 63)) & 1u, [] {});

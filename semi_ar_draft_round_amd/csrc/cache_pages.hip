@@ -325,10 +325,15 @@ __global__ __launch_bounds__(kT) void cache_fork_small(int R, int P, int n_pages
 }
 
 // Eviction, a work group a request: the k-th smallest mass of the pages that
-// may go is found a byte at a time from the top (four passes over keys, with
-// their counts in LDS), then the pages below it go, and of those equal to it
-// the first by entry.  Keys of up to kEvictPer a thread stay in registers, of
-// longer tables they are made again from memory in every pass.
+// may go is found a byte at a time from the top (at most four passes over keys,
+// their counts in LDS), as far down as it takes until all pages up to some key
+// go; then they do, and of equal masses that cannot all go the first by entry.
+// Keys of up to kEvictPer a thread stay in registers, of longer tables they are
+// made again from memory in every pass.
+//
+// The counts of one wave's keys meet in few places (masses share their
+// exponents), which LDS takes in turn; the loads and the released pages' writes
+// are what takes the time.
 constexpr int kEvictPer = 8;
 
 // Smaller mass, smaller key; -0 as 0, NaN above all.
@@ -336,15 +341,24 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return m != m ? 0xFFFFFFFFu : ordered_bits(m + 0.f);
 }
 
-template <bool LONG>
-__global__ __launch_bounds__(kT) void cache_evict_kernel(int R, int P, int n_pages, int max_pages, int sinks,
-                                                         int recent, const int32_t* budget, const int32_t* len,
-                                                         float* mass, int32_t* table, int32_t* ref, uint32_t* bits,
-                                                         int32_t* freed) {
-  __shared__ int lds[kT / 64];
+// As release, for a kernel in which counts only fall: a page that nobody else
+// holds (`holders`, read before) is nobody else's to count.
+__device__ __forceinline__ void release_own(int id, int holders, int32_t* ref, uint32_t* bits) {
+  if (holders == 1) ref[id] = 0;
+  else if (atomicSub(&ref[id], 1) != 1) return;
+  atomicOr(&bits[id >> 5], 1u << (id & 31));
+}
+
+template <int T, bool LONG>
+__global__ __launch_bounds__(T) void cache_evict_kernel(int P, int n_pages, int max_pages, int sinks, int recent,
+                                                        const int32_t* budget, const int32_t* len, float* mass,
+                                                        int32_t* table, int32_t* ref, uint32_t* bits, int32_t* freed) {
+  constexpr int W = T / 64;
+  __shared__ int2 sums[W];
   __shared__ int count[256];
-  __shared__ int s_digit, s_left;
+  __shared__ int s_digit, s_left, s_inside;
   const int r = blockIdx.x, most = budget[r];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t n = len[r];
   int32_t* row = table + static_cast<int64_t>(r) * max_pages;
   float* weight = mass + static_cast<int64_t>(r) * max_pages;
@@ -356,85 +370,118 @@ __global__ __launch_bounds__(kT) void cache_evict_kernel(int R, int P, int n_pag
   // entries that may go: first .. end - 1
   const int first = static_cast<int>(min((static_cast<int64_t>(sinks) + P - 1) / P, static_cast<int64_t>(used)));
   const int end = n > recent ? static_cast<int>(min((n - recent) / P, static_cast<int64_t>(used))) : 0;
-  const int rounds = ceil_div(used, kT);
-  bool may[kEvictPer];
+  const int rounds = ceil_div(used, T);
+  int id[kEvictPer];       // -1: may not go
   uint32_t key[kEvictPer];
   int held = 0, able = 0;
-  auto look = [&](int i, bool& can, uint32_t& k) {
-    const int s = i * kT + threadIdx.x;
-    const bool have = s < used && page_or_none(row[s], n_pages) >= 0;
-    can = have && s >= first && s < end;
-    k = can ? mass_key(weight[s]) : 0u;
-    return have;
+  auto look = [&](int i, int& page, uint32_t& k) {
+    const int s = i * T + threadIdx.x;
+    page = s < used ? page_or_none(row[s], n_pages) : -1;
+    const float m = s < used ? weight[s] : 0.f;
+    held += page >= 0;
+    if (s < first || s >= end) page = -1;
+    able += page >= 0;
+    k = mass_key(m);
   };
-  if constexpr (LONG) {
-    for (int i = 0; i < rounds; ++i) {
-      held += look(i, may[0], key[0]);
-      able += may[0];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kEvictPer; ++i) {
-      held += look(i, may[i], key[i]);
-      able += may[i];
-    }
-  }
-  block_exclusive_scan(held, lds, &held);
-  block_exclusive_scan(able, lds, &able);
-  const int k = min(held - most, able);
-  if (threadIdx.x == 0 && freed) freed[r] = max(k, 0);
-  if (k <= 0) return;
-  // every key below `prefix` goes, and `left` of those that equal it
-  uint32_t prefix = 0;
-  int left = k;
-#pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) count[threadIdx.x] = 0;
-    __syncthreads();
-    const uint32_t above = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    auto tally = [&](bool can, uint32_t x) {
-      if (can && (x & above) == prefix) atomicAdd(&count[(x >> shift) & 255], 1);
-    };
+  // f(round, page, key) for this thread's entries, all of one round at a time
+  auto all = [&](auto f) {
     if constexpr (LONG) {
+#pragma unroll 1
       for (int i = 0; i < rounds; ++i) {
-        look(i, may[0], key[0]);
-        tally(may[0], key[0]);
+        look(i, id[0], key[0]);
+        f(i, id[0], key[0]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kEvictPer; ++i) tally(may[i], key[i]);
-    }
-    __syncthreads();
-    const int c = threadIdx.x < 256 ? count[threadIdx.x] : 0;
-    int all;
-    const int before = block_exclusive_scan(c, lds, &all);
-    if (before < left && left <= before + c) s_digit = threadIdx.x, s_left = left - before;
-    __syncthreads();
-    prefix |= static_cast<uint32_t>(s_digit) << shift;
-    left = s_left;
-    __syncthreads();
-  }
-  int equal_before = 0;  // keys equal to prefix in the rounds so far
-  auto drop = [&](int i, bool can, uint32_t x) {
-    const bool tie = can && x == prefix;
-    int ties;
-    const int at = equal_before + block_exclusive_scan(tie, lds, &ties);
-    equal_before += ties;
-    if ((can && x < prefix) || (tie && at < left)) {
-      const int s = i * kT + threadIdx.x;
-      release(row[s], n_pages, ref, bits);
-      row[s] = kEvicted;
-      weight[s] = 0.f;
+      for (int i = 0; i < kEvictPer; ++i)
+        if (i < rounds) f(i, id[i], key[i]);
     }
   };
   if constexpr (LONG) {
-    for (int i = 0; i < rounds; ++i) {
-      look(i, may[0], key[0]);
-      drop(i, may[0], key[0]);
-    }
+    all([](int, int, uint32_t) {});
   } else {
 #pragma unroll
-    for (int i = 0; i < kEvictPer; ++i) drop(i, may[i], key[i]);
+    for (int i = 0; i < kEvictPer; ++i) look(i, id[i], key[i]);
+  }
+  auto sum = [](int p, int q) { return p + q; };
+  const int held_w = wave_scan(held, sum), able_w = wave_scan(able, sum);
+  if (lane == 63) sums[wave] = make_int2(held_w, able_w);
+  for (int i = threadIdx.x; i < 256; i += T) count[i] = 0;
+  __syncthreads();
+  held = able = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) held += sums[w].x, able += sums[w].y;
+  const int k = min(held - most, able);
+  if (threadIdx.x == 0 && freed) freed[r] = max(k, 0);
+  if (k <= 0) return;
+  // keys whose bits under `mask` are below `prefix` go, and `left` of those that
+  // equal it, which are `inside` in all
+  uint32_t prefix = 0, mask = 0;
+  int left = k, inside = able;
+#pragma unroll 1
+  for (int shift = 24; shift >= 0 && left < inside; shift -= 8) {
+    all([&](int, int page, uint32_t x) {
+      if (page >= 0 && (x & mask) == prefix) atomicAdd(&count[(x >> shift) & 255], 1);
+    });
+    __syncthreads();
+    if (wave == 0) {  // four counts a lane, cleared for the next pass
+      int c[4], before = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c[j] = count[lane * 4 + j];
+        before += c[j];
+        count[lane * 4 + j] = 0;
+      }
+      before = wave_scan(before, sum) - before;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (before < left && left <= before + c[j]) s_digit = lane * 4 + j, s_left = left - before, s_inside = c[j];
+        before += c[j];
+      }
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(s_digit) << shift;
+    mask |= 0xFFu << shift;
+    left = s_left;
+    inside = s_inside;
+  }
+  int before = 0;  // equal ones in the rounds so far
+  auto goes = [&](int page, uint32_t x) {
+    const uint32_t y = x & mask;
+    if (left == inside) return page >= 0 && y <= prefix;
+    const bool tie = page >= 0 && y == prefix;
+    const int incl = wave_scan(static_cast<int>(tie), sum);
+    __syncthreads();
+    if (lane == 63) sums[wave].x = incl;
+    __syncthreads();
+    int at = before + incl - tie;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < wave) at += sums[w].x;
+      before += sums[w].x;
+    }
+    return page >= 0 && (y < prefix || (tie && at < left));
+  };
+  auto drop = [&](int i, int page, int holders) {
+    const int s = i * T + threadIdx.x;
+    release_own(page, holders, ref, bits);
+    row[s] = kEvicted;
+    weight[s] = 0.f;
+  };
+  if constexpr (LONG) {
+    all([&](int i, int page, uint32_t x) {
+      if (goes(page, x)) drop(i, page, ref[page]);
+    });
+  } else {
+    // all counts on their way before the first is used
+    int holders[kEvictPer];
+    all([&](int i, int page, uint32_t x) {
+      if (!goes(page, x)) id[i] = -1;
+      holders[i] = id[i] >= 0 ? ref[id[i]] : 0;
+    });
+    all([&](int i, int page, uint32_t) {
+      if (page >= 0) drop(i, page, holders[i]);
+    });
   }
 }
 
@@ -551,12 +598,13 @@ hipError_t cache_commit_launch(int R, int gamma, int P, int n_pages, int max_pag
 hipError_t cache_evict_launch(int R, int P, int n_pages, int max_pages, int sinks, int recent, const int32_t* budget,
                               const int32_t* len, float* mass, int32_t* table, int32_t* ref, uint32_t* bits,
                               int32_t* freed, hipStream_t s) {
-  if (max_pages <= kEvictPer * kT)
-    cache_evict_kernel<false><<<R, kT, 0, s>>>(R, P, n_pages, max_pages, sinks, recent, budget, len, mass, table, ref,
-                                               bits, freed);
-  else
-    cache_evict_kernel<true><<<R, kT, 0, s>>>(R, P, n_pages, max_pages, sinks, recent, budget, len, mass, table, ref,
-                                              bits, freed);
+  auto launch = [&](auto kernel, int threads) {
+    kernel<<<R, threads, 0, s>>>(P, n_pages, max_pages, sinks, recent, budget, len, mass, table, ref, bits, freed);
+  };
+  // few entries: a small work group, whose barriers cost less
+  if (max_pages <= kEvictPer * 128) launch(cache_evict_kernel<128, false>, 128);
+  else if (max_pages <= kEvictPer * kT) launch(cache_evict_kernel<kT, false>, kT);
+  else launch(cache_evict_kernel<kT, true>, kT);
   return hipGetLastError();
 }
 

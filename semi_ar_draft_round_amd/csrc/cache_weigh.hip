@@ -19,7 +19,6 @@ namespace dspark {
 
 namespace {
 
-constexpr int W = 4;            // waves of a work group
 constexpr int kRowTiles = 2;    // row tiles of a wave
 constexpr int kRows = kRowTiles * kTile;
 constexpr int kRun = 64;        // chunks that a work group takes at a time, a lane each
@@ -37,6 +36,10 @@ struct WeighArgs {
   float keep;
   float* mass;
 };
+
+// Waves of a work group, one on a compute unit: as many as its registers hold
+// (256 dims: one a SIMD).
+constexpr int waves_of(int D) { return D == 256 ? 4 : 8; }
 
 // A request's chunks that any of its rows can see: 0 .. head - 1, then first
 // .., count in all; positions fit 32 bits.
@@ -72,9 +75,9 @@ __device__ __forceinline__ Span span_of(const WeighArgs& a, int r, int chunk) {
 
 // TWO: pages of 16 tokens, two a tile.
 template <int FMT, int D, bool TWO>
-__global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_weigh_kernel(WeighArgs a) {
+__global__ __launch_bounds__(waves_of(D) * 64) void cache_weigh_kernel(WeighArgs a) {
   typedef PageLayout<FMT, D> L;
-  constexpr int T = W * 64, KS = D / 16;
+  constexpr int W = waves_of(D), T = W * 64, KS = D / 16;
   __shared__ int64_t lds_cum[kCacheMaxR];  // units of requests 0 .. r
   __shared__ int64_t lds_scan[W];
   __shared__ float lds_sum[W][2 * kRun];
@@ -104,18 +107,6 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_weigh_kernel(W
   for (int r = r0; r < r1; ++r) lds_cum[r] += before;
   __syncthreads();
 
-  // entries that no row sees only fade
-  if (a.keep != 1.f) {
-    const int parts = ceil_div(a.max_pages, T);
-    for (int64_t x = blockIdx.x; x < static_cast<int64_t>(a.R) * parts; x += gridDim.x) {
-      const int r = static_cast<int>(x / parts), s = static_cast<int>(x % parts) * T + threadIdx.x;
-      const Span b = span_of(a, r, chunk);
-      const int c = (TWO ? s >> 1 : s);
-      if (b.n > 0 && s < a.max_pages && (s >= b.pages || (c >= b.head && c < b.first)))
-        a.mass[static_cast<int64_t>(r) * a.max_pages + s] *= a.keep;
-    }
-  }
-
   const int64_t share = quotient(N, gridDim.x), rest = N - share * gridDim.x;
   const int wg = blockIdx.x;
   const int64_t u0 = share * wg + (wg < rest ? wg : rest), u1 = u0 + share + (wg < rest ? 1 : 0);
@@ -142,7 +133,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_weigh_kernel(W
     const int64_t first_row = a.row0 ? static_cast<int64_t>(a.row0[r]) : static_cast<int64_t>(r) * (a.gamma + 1);
     const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
     // waves along the items (heads and row blocks), the others along the chunks
-    const int along = items >= 4 ? 4 : items >= 2 ? 2 : 1, across = W / along;
+    const int along = items >= W ? W : items >= 4 ? 4 : items >= 2 ? 2 : 1, across = W / along;
     const int wi = wave % along, wc = wave / along;
 #pragma unroll 1
     for (int run = c0; run < c1; run += kRun) {
@@ -239,8 +230,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_weigh_kernel(W
           }
           if ((k + 1) % tiles_per == 0) {  // the chunk's last tile
             if (!TWO) p0 += p1;
-            float x0 = wave_reduce_sum(p0), x1 = TWO ? wave_reduce_sum(p1) : 0.f;
-            if (lane == 0) {
+            const auto sum = [](float p, float q) { return p + q; };
+            const float x0 = wave_scan(p0, sum), x1 = TWO ? wave_scan(p1, sum) : 0.f;
+            if (lane == 63) {
               lds_sum[wave][c] += x0;
               if (TWO) lds_sum[wave][kRun + c] += x1;
             }
@@ -275,14 +267,26 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_weigh_kernel(W
       __syncthreads();
     }
   }
+
+  // entries that no row sees only fade: first those work groups that had no chunks
+  if (a.keep != 1.f) {
+    const int parts = ceil_div(a.max_pages, T);
+    for (int64_t x = gridDim.x - 1 - blockIdx.x; x < static_cast<int64_t>(a.R) * parts; x += gridDim.x) {
+      const int r = static_cast<int>(x / parts), s = static_cast<int>(x % parts) * T + threadIdx.x;
+      const Span b = span_of(a, r, chunk);
+      const int c = (TWO ? s >> 1 : s);
+      if (b.n > 0 && s < a.max_pages && (s >= b.pages || (c >= b.head && c < b.first)))
+        a.mass[static_cast<int64_t>(r) * a.max_pages + s] *= a.keep;
+    }
+  }
 }
 
 template <int FMT, int D>
 hipError_t run_p(WeighArgs& a, hipStream_t s) {
   a.page_bytes = a.Hkv * PageLayout<FMT, D>::head_bytes(a.P);
-  const int grid = compute_units() * (D == 256 ? 1 : 2);
-  if (a.P == 16) cache_weigh_kernel<FMT, D, true><<<grid, W * 64, 0, s>>>(a);
-  else cache_weigh_kernel<FMT, D, false><<<grid, W * 64, 0, s>>>(a);
+  const int grid = compute_units();
+  if (a.P == 16) cache_weigh_kernel<FMT, D, true><<<grid, waves_of(D) * 64, 0, s>>>(a);
+  else cache_weigh_kernel<FMT, D, false><<<grid, waves_of(D) * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -108,6 +108,17 @@ __global__ __launch_bounds__(kT) void logits_kernel(LogitsArgs a) {
   const int v0 = blockIdx.x * kSlice + threadIdx.x * kEach;
   const int n = max(0, min(kEach, a.V - v0));
   const int64_t row0 = a.row0 ? static_cast<int64_t>(a.row0[r]) : static_cast<int64_t>(r) * (a.gamma + 1);
+  // a row's logits and mask are on their way while the row before is worked on
+  auto load_row = [&](int i, Logits& y, uint32_t& allowed) {
+    const int64_t row = row0 + i;
+    if (n > 0) {
+      y.load(static_cast<const S*>(a.in) + row * a.V + v0, n);
+      allowed = a.mask ? a.mask[row * a.mask_row + (v0 >> 3)] : 0xFFu;
+    }
+  };
+  Logits next{};
+  uint32_t next_allowed = 0xFFu;
+  load_row(i0, next, next_allowed);
   // the tokens that rows follow: the anchor, the drafts
   if (a.state)
     for (int j = threadIdx.x; j < i1; j += kT)
@@ -136,10 +147,11 @@ __global__ __launch_bounds__(kT) void logits_kernel(LogitsArgs a) {
   for (int j = 0; j < a.nb; j += 64) {
     const int64_t at = static_cast<int64_t>(r) * a.nb + j + lane;
     const int tok = j + lane < a.nb ? token_or_none(a.bias_tok[at], a.V) : -1;
+    const float value = j + lane < a.nb ? a.bias[at] : 0.f;
     for (uint64_t here = __ballot(tok >= slice0 && tok < slice0 + kSlice); here; here &= here - 1) {
       const int l = __builtin_ctzll(here);
       const int t = __builtin_amdgcn_readlane(tok, l);
-      const float b = a.bias[static_cast<int64_t>(r) * a.nb + j + l];
+      const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), l));
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (t == v0 + e) bias[e] += b;
@@ -156,10 +168,9 @@ __global__ __launch_bounds__(kT) void logits_kernel(LogitsArgs a) {
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const int64_t row = row0 + i;
-    Logits in;
-    in.load(static_cast<const S*>(a.in) + row * a.V + v0, n);
-    uint32_t allowed = 0xFFu;
-    if (a.mask) allowed = a.mask[row * a.mask_row + (v0 >> 3)];
+    const Logits in = next;
+    const uint32_t allowed = next_allowed;
+    if (i + 1 < i1) load_row(i + 1, next, next_allowed);
     if (a.state) {
       const int t = lds_tok[i];
 #pragma unroll
@@ -192,9 +203,14 @@ __global__ __launch_bounds__(kT) void logits_prompt_kernel(int V, int64_t n, con
   const int64_t last = min(static_cast<int64_t>(start[r]) + m, n);
   for (int i = threadIdx.x; i < kPromptSlice / 32; i += kT) seen[i] = 0;
   __syncthreads();
-  for (int64_t i = first + threadIdx.x; i < last; i += kT) {
-    const int t = tokens[i];
-    if (t >= v0 && t < v0 + kPromptSlice) atomicOr(&seen[(t - v0) >> 5], 1u << (t & 31));
+  constexpr int kAtOnce = 8;
+  for (int64_t i = first + threadIdx.x; i < last; i += kAtOnce * kT) {
+    int t[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) t[j] = i + j * kT < last ? tokens[i + j * kT] : -1;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (t[j] >= v0 && t[j] < v0 + kPromptSlice) atomicOr(&seen[(t[j] - v0) >> 5], 1u << (t[j] & 31));
   }
   __syncthreads();
   uint16_t* p = state + static_cast<int64_t>(r) * V;
