@@ -588,7 +588,7 @@ def dspark_cache_workspace_size(kind: int, R: int, gamma: int, a: int, b: int, c
 def _raw_stream(dev: int) -> int:
     """The current stream of device `dev`, which must be the current device:
     cache calls run there, and tensors of another device are refused."""
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():  # (a tensor is on a GPU: it is initialised)
         raise ValueError(f"tensors are on device {dev} (-1: the CPU), not on the current GPU")
     return torch._C._cuda_getCurrentRawStream(dev)
 
@@ -601,7 +601,7 @@ def _need(t, name, shape, dtype, dev: int):
     return t.data_ptr()
 
 
-_I32, _BF, _U8 = torch.int32, torch.bfloat16, torch.uint8
+_I32, _BF, _U8, _F32 = torch.int32, torch.bfloat16, torch.uint8, torch.float32
 
 
 def _cache_ws(ws, kind, R, gamma, a, b, c, dev):
@@ -915,8 +915,9 @@ def dspark_logits(logits, state, ell, gamma, x0, x=None, *, row0=None, repetitio
     p_state = None if state is None else _state(state, R, V, dev)
     p_x0 = None if x0 is None else _need(x0, "x0", (R,), _I32, dev)
     p_x = _drafts(x, R, gamma, dev)
-    per = [None if t is None else _need(t, n, (R,), torch.float32, dev)
-           for t, n in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency"))]
+    p_rep = None if repetition is None else _need(repetition, "repetition", (R,), _F32, dev)
+    p_pres = None if presence is None else _need(presence, "presence", (R,), _F32, dev)
+    p_freq = None if frequency is None else _need(frequency, "frequency", (R,), _F32, dev)
     nb, p_tok, p_bias = 0, None, None
     if (bias_tok is None) != (bias is None):
         raise ValueError("bias_tok and bias come together")
@@ -930,8 +931,8 @@ def dspark_logits(logits, state, ell, gamma, x0, x=None, *, row0=None, repetitio
     stream = _raw_stream(dev)
     if rows == 0:
         return out
-    st = load_library().dspark_logits(_dt(logits), R, gamma, V, p_in, p_row0, p_ell, p_x0, p_x, p_state, *per, nb,
-                                      p_tok, p_bias, p_mask, p_out, stream)
+    st = load_library().dspark_logits(_dt(logits), R, gamma, V, p_in, p_row0, p_ell, p_x0, p_x, p_state, p_rep,
+                                      p_pres, p_freq, nb, p_tok, p_bias, p_mask, p_out, stream)
     _raise("dspark_logits", st)
     return out
 

@@ -17,6 +17,14 @@
 // A code is rounded once: fp64 is cut to fp32 with what was cut off kept in
 // the last bit (a value between two codes, or between a code and the border
 // beside it, stays there), and the conversion rounds that.
+//
+// What bounds it is latency: the length, the page's id, the rows and the block's
+// codes are loads one after another, and a block's bounds need all of its rows.
+// With 8 heads of keys of 128 dims: one token, 32 query heads, 4.5 .. 5.1 us;
+// 128 requests of up to 17 packed rows, 56 query heads, 22 .. 24 us, 31 MB, and
+// 31 with the read of their page tables after them.  Those took 40 with a wave
+// for a head and all its rows, in fp64 also where there are none, and 43 with
+// contiguous runs of tasks instead of every y-th.
 #include "cache_rows.hpp"
 
 namespace dspark {
@@ -284,7 +292,9 @@ __global__ __launch_bounds__(2 * D) void cache_append8_kernel(AppendArgs a) {
   }
 }
 
-// Work groups of a compute unit that are asked for.
+// Work groups of a compute unit that are asked for.  With their read, 128 x up
+// to 17 packed rows take 31.3, 30.6, 30.9 and 30.9 us with 4, 6, 8 and 12, 4 x
+// 512 rows 27.8, 28.8, 28.4, 29.8, 32 x 17 rows 17.1, 17.6, 19.7, 20.9.
 constexpr int64_t kPerUnit = 6;
 
 template <int D>

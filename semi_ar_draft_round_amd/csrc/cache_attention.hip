@@ -14,8 +14,13 @@
 //                  tokens together, which is the A operand.
 // Pages hold both operands in 16-byte pieces, contiguous over the lanes that
 // read them, so a tile goes straight into registers where every wave has
-// tiles of its own (rows of one row tile; 4 bits), and past the registers into
-// a ring in LDS where several waves multiply the same 16-bit tile.
+// tiles of its own (rows of one row tile; 4 bits; 8 bits up to 128 dims), and
+// past the registers into a ring in LDS where several waves multiply the same
+// 16-bit tile, and for 8-bit heads of 256 dims, whose one wave a SIMD has no
+// registers to load ahead (32 single tokens over 8192 165 us straight, 101 so;
+// 16 x 17 rows 185 and 119).  8-bit tiles of shorter heads in the ring measured
+// no gain (the ragged 128 requests 607 and 606 us, 32 x 17 rows over 4096 93 and
+// 84).
 //
 // Work is split over tokens as well as rows.  The units (request, row block,
 // head, tile) are numbered in that order, and every work group takes a
@@ -32,7 +37,9 @@
 // 97 us, 3.7 TB/s).  Many rows of 4 bits (the same 128 requests up to 16384
 // tokens 505 us) are bound by the order inside a wave: vector instructions
 // take 47 % of the issue slots and products 33 % of the matrix units' time,
-// and with two waves a SIMD neither hides the other whole.  Heads of 256 dims
+// and with two waves a SIMD neither hides the other whole; of 8 bits the same
+// requests take 607 us (4.3 TB/s; 47 % and 36 %), 32 single tokens over 16384
+// tokens 137 us, 5.0 TB/s.  Heads of 256 dims
 // have one wave a SIMD, where nothing but the wave itself does; 65 .. 96 query
 // rows are three row tiles, and the fourth wave of the work group idles.
 // Short contexts are bound by the two launches and the chain of loads before
@@ -86,8 +93,10 @@ struct Block {
 };
 // Units of a tile by the log2 of the waves along the rows: the time it takes.
 // 16-bit tiles come at the pace of memory until four waves share them; 4-bit
-// ones at that of the vector units nearly from the start.  Measured with heads
-// of 128 dims, as kRestart and kFavour below.
+// ones at that of the vector units nearly from the start, and 8-bit ones too
+// (the ragged 128 requests over them 606 us; with 2, 4, 6 630, with 2, 3, 6 616,
+// with the weights of 16 bits 730).  Measured with heads of 128 dims, as
+// kRestart and kFavour below.
 __device__ __forceinline__ int weight_of(int fmt, int shift) {
   return fmt == DSPARK_CACHE_BF16 ? 2 + shift : (shift == 0 ? 2 : shift == 1 ? 4 : 7);
 }
@@ -297,7 +306,8 @@ constexpr int kRestart = 16;
 // more, in 64ths of an equal share: 545 -> 511 us for 128 requests x up to 17
 // rows over ragged contexts up to 16384, 142 -> 135 us for 32 x 17 rows over
 // 8192.  At the pace of memory it makes no difference (16-bit pages: within 1
-// %), and short runs lose: only from 4 kMinUnits a work group on.
+// %; 8-bit ones 608 -> 606 us, 601 with 4, 631 with 12), and short runs lose:
+// only from 4 kMinUnits a work group on.
 constexpr int kFavour = 7;
 
 // A head in `parts` parts of `tiles` tiles, the last ones perhaps empty; with
@@ -339,7 +349,9 @@ struct Deal {
 
 // Waves along the tokens by the log2 of those along the rows.  Of 16-bit
 // heads of 256 dims no tile fits the registers beside the output, so theirs
-// all come through LDS, and the ring there holds two rounds of two.
+// all come through LDS, and the ring there holds two rounds of two; 8-bit ones
+// come through it too, half as large: two rounds of four (32 single tokens over
+// 8192 101 us, 124 with two along the tokens).
 __device__ __forceinline__ int waves_along(int fmt, int D, int shift) {
   return fmt == DSPARK_CACHE_BF16 && D == 256 ? min(2, W >> shift) : W >> shift;
 }
