@@ -14,8 +14,9 @@ With a budget of pages, attend also weighs the pages and commit lets go of
 those that got least attention.
 
 Nothing is allocated after construction except output tensors and the
-attention's workspace where the caller does not pass them, from torch's
-allocator, so a round can be captured in a HIP graph.  All calls run on the
+attention's workspace where the caller does not pass them, and what fork needs
+for a moment, from torch's allocator, so a round can be captured in a HIP
+graph.  All calls run on the
 current stream.
 """
 
@@ -44,8 +45,9 @@ class PagedCache:
         so that commit can release what no later row sees.  budget: pages a
         request may keep after a commit (None: all; self.budget [slots] holds
         it, so that requests can have their own): those whose tokens got the
-        least attention go, never the first keep_first and the last keep_last
-        tokens'; earlier rounds count `fade` times as much with every round."""
+        least attention go, never the first keep_first (or sinks, if these are
+        more) and the last keep_last tokens'; earlier rounds count `fade` times
+        as much with every round."""
         dev = torch.device(device)
         nb = B.dspark_cache_page_bytes(fmt, heads_kv, dim, page)
         if nb == 0 or layers < 1 or slots < 1 or max_tokens < 1 or n_pages < 1:
@@ -131,7 +133,7 @@ class PagedCache:
                               page=self.page, window=self.window, sinks=self.sinks)
         if self.budget is not None:
             B.dspark_cache_evict(self.table, self.length, self.ref, self.bits, self.mass, self.budget, page=self.page,
-                                 sinks=self.keep_first, recent=self.keep_last, freed=self.freed)
+                                 sinks=max(self.keep_first, self.sinks), recent=self.keep_last, freed=self.freed)
 
     def fork(self, parent):
         """Request r takes over parent[r]'s tokens, shared (r: stays; -1: empty)."""

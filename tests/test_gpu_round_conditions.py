@@ -147,3 +147,20 @@ def test_fork_takes_weights_along(dev):
     assert c.mass.tolist() == [[float(x) for x in range(14, 21)], [0.0] * 7, [float(x) for x in range(14, 21)]]
     c.reset()
     assert not c.mass.any()
+
+
+def test_a_budget_leaves_the_windows_first_tokens(dev):
+    """What the attention's window keeps visible is not evicted, whether or not
+    it got any weight."""
+    from semi_ar_draft_round_amd.cache import PagedCache
+    say("[round] budget and window")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+    c = PagedCache(1, 2, 300, 40, 1, 64, page=16, window=64, sinks=20, budget=3)
+    x = torch.ones((2 * 100, 1, 64), dtype=torch.bfloat16, device=dev)
+    c.reserve(i32([99, 99]), 99)
+    c.attend(0, c.append(0, x, x, x))
+    c.mass.copy_(torch.arange(c.mass.shape[1], device=dev).expand(2, -1))
+    c.commit(i32([99, 70]))
+    torch.cuda.synchronize()
+    assert (c.table[:, :2] >= 0).all()
+    assert [(row >= 0).sum().item() for row in c.table] == [3, 3]
