@@ -384,3 +384,45 @@ def test_captured_and_on_another_stream(dev):
         torch.cuda.synchronize()
         k1, v1 = c.read(1, 40)
         assert torch.equal(o[:6], out[:6]) and torch.equal(n, c.length) and torch.equal(rk, k1) and torch.equal(rv, v1)
+
+
+def test_forked_blocks_and_moved_pages(dev):
+    """A block that requests share and then go on with apart (its scales grow in
+    the copies, not in the page the others read), and pages drawn together: as
+    if every request had appended all of it itself."""
+    from semi_ar_draft_round_amd.cache import PagedCache
+    say("[cache8] forked")
+    g = torch.Generator().manual_seed(11)
+    D, n0, gamma = 64, 21, 24
+    draw = lambda n, s: [(torch.randn((n, 2, D), generator=g) * s).to(torch.bfloat16).to(dev) for _ in range(2)]
+    k0, v0 = draw(n0, 1.0)
+    k1, v1 = draw(3 * (gamma + 1), 4000.0)
+    q = torch.ones((3 * (gamma + 1), 2, D), dtype=torch.bfloat16, device=dev)
+    forked, apart = (PagedCache(1, 3, 100, 14, 2, D, page=32, fmt=FP8) for _ in range(2))
+
+    def append(c, ell, k, v):
+        c.reserve(i32(ell, dev), gamma)
+        assert c.ell.tolist() == ell
+        c.append(0, q, k, v)
+        c.commit(i32([max(e, 0) for e in ell], dev))
+
+    def first(c, ell):
+        k, v = (torch.zeros((3, gamma + 1, 2, D), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        k[:, :n0], v[:, :n0] = k0, v0
+        append(c, ell, k.view(-1, 2, D), v.view(-1, 2, D))
+
+    first(forked, [n0 - 1, -1, -1])
+    first(apart, [n0 - 1] * 3)
+    forked.fork(i32([0, 0, 0], dev))
+    for c in (forked, apart):
+        append(c, [0, 5, -1], k1, v1)
+    k, v = forked.read(0, 60)
+    assert all(torch.equal(a, b) for a, b in zip((k, v), apart.read(0, 60)))
+    assert not torch.equal(k[0, :n0], k[2, :n0])          # the larger scale has cost slot 0's copy its small values
+    for c in (forked, apart):
+        append(c, [17, 24, 2], k1, v1)
+        c.fork(i32([-1, 1, 2], dev))
+        c.compact()
+        append(c, [3, 0, 4], k1, v1)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(forked.read(0, 60), apart.read(0, 60)))
