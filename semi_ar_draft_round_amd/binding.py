@@ -894,11 +894,12 @@ def _drafts(x, R, gamma, dev):
 def dspark_logits(logits, state, ell, gamma, x0, x=None, *, row0=None, repetition=None, presence=None, frequency=None,
                   bias_tok=None, bias=None, mask=None, out=None):
     """out (a new tensor, or given, also logits itself; rows of nobody are not
-    written): the rows' logits with penalties, biases and masks.  logits [rows][V] or, without row0, [R][gamma +
-    1][V]; state [R][V] int16 (None: no penalties); x0 [R], x [R][gamma] int32;
-    repetition, presence, frequency [R] float32; bias_tok [R][n] int32 with bias
-    [R][n] float32; mask [rows][ceil(V / 32)] int32, bit v % 32 of word v / 32
-    set where v is allowed."""
+    written): the rows' logits with penalties, biases and masks.  logits
+    [rows][V] or, without row0, [R][gamma + 1][V]; state [R][V] int16 (None: no
+    penalties); x0 [R], x [R][gamma] int32; repetition, presence, frequency [R]
+    float32; bias_tok [R][n] int32 with bias [R][n] float32; mask
+    [rows][ceil(V / 32)] int32, bit v % 32 of word v / 32 set where v is
+    allowed."""
     dev = logits.get_device()
     if logits.dim() not in (2, 3) or (logits.dim() == 3 and row0 is not None):
         raise ValueError("logits must be [rows][V], or [R][gamma + 1][V] without row0")

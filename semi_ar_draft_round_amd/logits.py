@@ -11,7 +11,7 @@ points in a round's order:
 device_round.run_round_cached does the last two.  The tensors `repetition`,
 `presence`, `frequency` [slots], `bias_tok` and `bias` [slots][biases] are the
 caller's to fill (a bias_tok of -1 is none); they start without effect.
-Nothing is allocated after construction except an output that is not passed,
+Nothing is allocated after construction except what fork needs for a moment,
 so a round can be captured in a HIP graph.  All calls run on the current
 stream.
 """
