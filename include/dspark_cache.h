@@ -186,10 +186,10 @@ dspark_status dspark_cache_attention(int fmt, int R, int gamma, int Hq, int Hkv,
  *
  * Token start[r] + i, i < min(count[r], T), goes to k[r][i] and v[r][i]
  * ([Hkv][D]); other rows are left as they were, tokens without a page read as
- * zero.  4-bit values are exact in bf16 for K, and rounded once for V.
+ * zero.  8-bit values are exact in bf16, 4-bit values for K, and rounded once
+ * for V.
  *
  *   start NULL: 0.  Limits: as append; 1 <= T <= 2^26.
- * 8-bit values are exact in bf16.
  */
 dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, int n_pages, int max_pages,
                                 const int32_t* start, const int32_t* count, const int32_t* table, const void* pool,
@@ -201,9 +201,9 @@ dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, in
  *   mass[r][s] <- keep * mass[r][s] + sum exp(scale * q . k_j - lse)
  * over the rows, the query heads and the tokens j of page s that the row sees
  * (dspark_cache_attention's rule and its lse).  Requests without rows are left
- * as they were.  Every row and head shares out 1 over
- * the pages it sees.  Drafts count whether they are accepted or not; called
- * with n_acc in the place of ell, before commit, only the rows that stay do.
+ * as they were.  Every row and head shares out 1 over the pages it sees.  Drafts
+ * count whether they are accepted or not; called with n_acc in the place of ell,
+ * before commit, only the rows that stay do.
  * The layers of a model share a table, so a round calls it once per layer with
  * one mass: keep < 1 (older rounds fade) for the first, 1 for the others.
  *
@@ -244,11 +244,11 @@ dspark_status dspark_cache_reset(int R, int n_pages, int max_pages, int32_t* tab
 /*
  * dspark_cache_reserve — pages for rows len[r] .. len[r] + ell[r].
  *
- * Entries that are no page get new pages.  If the page that holds token len[r] - 1
- * is also to be written (len[r] % P != 0) and other requests hold it too, r
- * gets a copy of it instead: pairs gets (old, new), and the old page loses a
- * reference; of several such requests of one call the last keeps the old page
- * if nobody else holds it.  ell_out[r] = ell[r], or -1 for a request that was
+ * Entries that are no page get new pages.  If the page that holds token
+ * len[r] - 1 is also to be written (len[r] % P != 0) and other requests hold it
+ * too, r gets a copy of it instead: pairs gets (old, new), and the old page
+ * loses a reference; of several such requests of one call the last keeps the
+ * old page if nobody else holds it.  ell_out[r] = ell[r], or -1 for a request that was
  * refused: its rows would pass max_pages, or the free pages were used up by
  * the requests before it (then every later request that needs pages, or whose
  * page an earlier one should have left, is refused too); nothing of a refused

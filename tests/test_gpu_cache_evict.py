@@ -107,10 +107,11 @@ def test_evict_against_oracle(P, sinks, recent, kind, dev):
 
 
 def test_long_tables(dev):
-    """Tables past what a thread keeps in registers, and whose length is just that."""
+    """Tables past what a thread keeps in registers or a work group of either
+    size takes, and whose length is just that."""
     say("[evict] long tables")
     rng = np.random.default_rng(3)
-    for M, lens in ((8192, [16 * 8192, 16 * 8000 - 5]), (8193, [16 * 8193, 16 * 3]), (30000, [16 * 30000 - 9, 16 * 29000])):
+    for M, lens in ((512, [16 * 512, 16 * 500 - 5]), (513, [16 * 513, 16 * 300]), (1025, [16 * 1025, 16]), (8192, [16 * 8192, 16 * 8000 - 5]), (8193, [16 * 8193, 16 * 3]), (30000, [16 * 30000 - 9, 16 * 29000])):
         p = filled(rng, lens, 16, M)
         s = State(p, dev)
         for kind, budget in (("ties", [M // 2, 2]), ("odd", [100, 7]), ("plain", [0, 0])):

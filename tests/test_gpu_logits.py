@@ -133,7 +133,8 @@ class Case:
 @pytest.mark.parametrize("R,gamma,V,ells,packed", [(1, 0, 2, [0], False), (1, 4, 7, [4], True), (3, 4, 1024, [4, -1, 2], True),
                                                    (2, 16, 2047, [16, 9], False), (5, 2, 2049, [0, 5, -3, 2, 1], False),
                                                    (2, 3, 5003, [3, 3], True), (4, 1, 33000, [1, 0, -1, 1], True),
-                                                   (1, 200, 301, [200], True)])
+                                                   (1, 200, 301, [200], True), (1, 1023, 40, [1023], False),
+                                                   (300, 2, 50, [r % 4 - 1 for r in range(300)], True)])
 def test_logits_against_oracle(R, gamma, V, ells, packed, dt, dev):
     say(f"[logits] {dt} {R} {gamma} {V}")
     Case(dev, dt, R, gamma, V, ells, packed, seed=V).check()
@@ -170,7 +171,7 @@ def test_not_finite_logits_and_rows_that_allow_nothing(dev):
     assert np.all(c.call(c.x, torch.empty_like(c.x)).cpu().numpy() == -np.inf)   # NaN and inf too
 
 
-@pytest.mark.parametrize("V", [2, 31, 1000, 16384, 16385, 40007])
+@pytest.mark.parametrize("V", [2, 31, 1000, 8191, 8192, 8193, 16384, 16385, 40007])
 def test_history(V, dev):
     """Prompts of every length, slots left alone, rounds with repeated tokens."""
     from semi_ar_draft_round_amd.logits import Conditions
