@@ -39,9 +39,9 @@
 // take 47 % of the issue slots and products 33 % of the matrix units' time,
 // and with two waves a SIMD neither hides the other whole; of 8 bits the same
 // requests take 607 us (4.3 TB/s; 47 % and 36 %), 32 single tokens over 16384
-// tokens 137 us, 5.0 TB/s.  Heads of 256 dims
-// have one wave a SIMD, where nothing but the wave itself does; 65 .. 96 query
-// rows are three row tiles, and the fourth wave of the work group idles.
+// tokens 137 us, 5.0 TB/s.  Heads of 256 dims have one wave a SIMD, where
+// nothing but the wave itself does; 65 .. 96 query rows are three row tiles, and
+// the fourth wave of the work group idles.
 // Short contexts are bound by the two launches and the chain of loads before
 // the first tile, 6 of 13 us (one token over 1023).
 #include "cache_tiles.hpp"
@@ -392,7 +392,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
   // far from overflow as those of a plain softmax, and few tiles rescale.
   constexpr float kSlack = 8.f;
   constexpr bool kShared = FMT == DSPARK_CACHE_BF16 || (FMT == DSPARK_CACHE_FP8 && D == 256);
-  // the waves' outputs, on their way to be joined; before that the ring of 16-bit tiles
+  // the waves' outputs, on their way to be joined; before that the ring of tiles
   __shared__ f32x4 lds_own[W][NB * 4][64];
   __shared__ float2 lds_ml[W][64];
   static_assert((NB * 4) % W == 0, "waves share an output's pieces");
@@ -883,9 +883,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : 2) void cache_attention_tile
       // tiles leave room for the next one's scores, whose products then run
       // beside this one's exponentials (128 requests x up to 17 rows over
       // ragged contexts up to 16384: 550 -> 511 us with it; 64 x 17 rows, heads
-      // of 256 dims, up to 4096: 363 -> 322).  8-bit tiles come at the pace of
-      // memory, and the registers that this takes cost them (32 tokens over
-      // 16384 tokens 152 us with it, 136 without; the 128 requests 617 and 606).
+      // of 256 dims, up to 4096: 363 -> 322).  8-bit tiles take more registers,
+      // and loads ahead are worth more to them (32 tokens over 16384 tokens 152
+      // us with scores ahead, 136 without; the 128 requests 617 and 606).
       constexpr bool kAhead = FMT == DSPARK_CACHE_FP4;
       const int steps = uniform((tiles - wt + WT - 1) >> (__ffs(WT) - 1));
       const int k_token = (TWO ? 0 : col & 16) + token_of_slot(col & 15);
