@@ -821,6 +821,11 @@ __global__ __launch_bounds__(256) void acceptance_finish(int rows, int parts, co
 // vectors into registers (a run of 4 kSelVec per thread), scanned per wave and
 // across the waves; the chunk's Markov biases are dot products split over
 // sixteen threads per token against the previous token's W1 row in LDS.
+//
+// A token without mass (one that a mask forbids) is never drawn.  The scan and
+// a thread's own sums round differently, so u * Z can lie below where the
+// thread it falls to begins: that thread's first chunk with mass holds it, and
+// there the first token with mass.
 template <typename Elt>
 __global__ __launch_bounds__(256) void verify_select(
     int R, int gamma, int V, int r, const typename Elt::T* __restrict__ target,
@@ -906,7 +911,7 @@ __global__ __launch_bounds__(256) void verify_select(
       last = cc;
       last_before = run;
     }
-    if (first == 0x7FFFFFFF && run + sv > thr) {
+    if (first == 0x7FFFFFFF && sv > 0.f && run + sv > thr) {
       first = cc;
       before = run;
     }
@@ -959,7 +964,7 @@ __global__ __launch_bounds__(256) void verify_select(
   if (tid < kWave) {
     const float val = tid < kGChunk ? s_val[tid] : 0.f;
     const float cum = wave_inclusive_scan(val);
-    const unsigned long long hit = __ballot(tid < kGChunk && cum > thr - base);
+    const unsigned long long hit = __ballot(val > 0.f && cum > fmaxf(thr - base, 0.f));
     int off;
     if (hit) {
       off = __ffsll(static_cast<long long>(hit)) - 1;
