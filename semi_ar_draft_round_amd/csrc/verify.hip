@@ -825,7 +825,10 @@ __global__ __launch_bounds__(256) void acceptance_finish(int rows, int parts, co
 // A token without mass (one that a mask forbids) is never drawn.  The scan and
 // a thread's own sums round differently, so u * Z can lie below where the
 // thread it falls to begins: that thread's first chunk with mass holds it, and
-// there the first token with mass.
+// there the first token with mass.  A chunk's mass and its tokens' are computed
+// in different ways, so that a mass of roundings may be there in one and in the
+// other not: then the token whose p_t is furthest above its p_d is drawn, of
+// those that the target does not rule out.
 template <typename Elt>
 __global__ __launch_bounds__(256) void verify_select(
     int R, int gamma, int V, int r, const typename Elt::T* __restrict__ target,
@@ -839,7 +842,7 @@ __global__ __launch_bounds__(256) void verify_select(
   constexpr int kSelVec = 12;
   __shared__ float wsum[kT / kWave];
   __shared__ float e_row[1024];
-  __shared__ float s_val[kGChunk];
+  __shared__ float s_val[kGChunk], s_over[kGChunk];
   __shared__ int s_chunk, s_last;
   __shared__ float s_before, s_last_before;
   const int req = blockIdx.x;
@@ -953,24 +956,29 @@ __global__ __launch_bounds__(256) void verify_select(
 #pragma unroll
   for (int o = 1; o < kGChunk; o <<= 1) b += __shfl_xor(b, o);
   if (sl == 0) {
-    float val = 0.f;
+    float val = 0.f, over = neg_inf();
     if (v < V) {
       const float pt = __expf(tl - rr.lt);
-      val = use_pt ? pt : fmaxf(0.f, pt - __expf(ul + b - rr.ld));
+      const float d = use_pt ? pt : pt - __expf(ul + b - rr.ld);
+      val = use_pt ? pt : fmaxf(0.f, d);
+      if (tl > neg_inf()) over = d;
     }
     s_val[tk] = val;
+    s_over[tk] = over;
   }
   __syncthreads();
   if (tid < kWave) {
     const float val = tid < kGChunk ? s_val[tid] : 0.f;
     const float cum = wave_inclusive_scan(val);
     const unsigned long long hit = __ballot(val > 0.f && cum > fmaxf(thr - base, 0.f));
-    int off;
+    int off = 0;
     if (hit) {
       off = __ffsll(static_cast<long long>(hit)) - 1;
+    } else if (const unsigned long long pos = __ballot(val > 0.f)) {
+      off = 63 - __clzll(static_cast<long long>(pos));
     } else {
-      const unsigned long long pos = __ballot(val > 0.f);
-      off = pos ? 63 - __clzll(static_cast<long long>(pos)) : 0;
+      for (int q = 1; q < kGChunk; ++q)
+        if (s_over[q] > s_over[off]) off = q;
     }
     if (tid == 0) next_tok[req] = chunk * kGChunk + off;
   }

@@ -89,6 +89,32 @@ def test_borders_between_threads(V, dtype, dev):
     assert bad == 0
 
 
+@pytest.mark.parametrize("V,dtype", [(16384, torch.bfloat16), (20000, torch.float32), (129280, torch.bfloat16)])
+def test_a_residual_of_roundings(V, dtype, dev):
+    """Target and draft alike but for the last bits of the draft's log-sum: what
+    is left of a chunk is rounding, and which of its tokens have some differs
+    between the sums and the draw."""
+    say(f"[verify] roundings {V} {dtype}")
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy((rng.standard_normal(V) * 2).astype(np.float32)).to(dtype)
+    # one token allowed in a chunk, never its first
+    allowed = np.zeros(-(-V // 16) * 16, bool)
+    allowed[np.arange(0, len(allowed), 16) + rng.integers(1, 16, len(allowed) // 16)] = True
+    allowed = allowed[:V]
+    row = x.clone()
+    row[torch.from_numpy(~allowed)] = -float("inf")
+    z = np.float32(torch.logsumexp(row.double(), 0).item())
+    R = 2048
+    U = row.to(dev)[None, None].expand(R, 1, V).contiguous()
+    lse = (np.full(R, z).view(np.int32) + np.arange(R) % 4 - 1).astype(np.int32).view(np.float32)
+    u = ((np.arange(R) + 0.5) / R).astype(np.float32)
+    tok = draw(dev, row, u, admitted=1, U=U, lse=torch.from_numpy(lse)[:, None].contiguous().to(dev),
+               logit=torch.full((R, 1), 1e4, device=dev))
+    bad = int((~allowed[tok]).sum())
+    say(f"  {len(u)} draws, {bad} of a forbidden token")
+    assert bad == 0
+
+
 @pytest.mark.parametrize("V,dtype", [(16384, torch.bfloat16), (20003, torch.float32)])
 def test_rows_that_allow_one_token_or_none(V, dtype, dev):
     say(f"[verify] one token {V} {dtype}")
