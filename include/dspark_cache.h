@@ -206,6 +206,11 @@ dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, in
  * before commit, only the rows that stay do.
  * The layers of a model share a table, so a round calls it once per layer with
  * one mass: keep < 1 (older rounds fade) for the first, 1 for the others.
+ * The entries of rejected drafts are weighed like the others, and no other call
+ * but dspark_cache_evict writes mass: after dspark_cache_commit the caller sets
+ * it to 0 where the table has no page, or a later page of that entry would start
+ * with what the released one got, and after dspark_cache_fork it moves rows of
+ * mass as the call moved rows of the table.
  *
  * Scores and sums are fp32, the sum in an order that follows from the batch
  * (the same call gives the same bits).  What an invisible token holds has no

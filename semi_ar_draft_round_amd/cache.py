@@ -83,6 +83,7 @@ class PagedCache:
             self.budget = torch.full((slots,), budget, **i32)
             self.mass = torch.zeros((slots, max_pages), dtype=torch.float32, device=dev)
             self.freed = torch.zeros(slots, **i32)   # pages that the last commit let go
+            self.vacant = torch.zeros((slots, max_pages), dtype=torch.bool, device=dev)
         self.reset()
 
     def reset(self):
@@ -132,6 +133,9 @@ class PagedCache:
         B.dspark_cache_commit(self.table, self.length, self.ref, self.bits, self.ell, n_acc, self.gamma,
                               page=self.page, window=self.window, sinks=self.sinks)
         if self.budget is not None:
+            # pages that the commit released: what they got is not the next ones' there
+            torch.lt(self.table, 0, out=self.vacant)
+            self.mass.masked_fill_(self.vacant, 0)
             B.dspark_cache_evict(self.table, self.length, self.ref, self.bits, self.mass, self.budget, page=self.page,
                                  sinks=max(self.keep_first, self.sinks), recent=self.keep_last, freed=self.freed)
 

@@ -1,0 +1,76 @@
+"""The masses that PagedCache keeps with a budget: each is what its page's tokens
+got, through commits, evictions and forks."""
+
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from semi_ar_draft_round_amd import binding
+    binding.load_library()
+    return torch.device("cuda:0")
+
+
+D, HQ, GAMMA, P = 64, 4, 20, 16
+
+
+class Rows:
+    """Rows by request and position, whatever round brings them."""
+
+    def __init__(self, dev, slots, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.x = torch.randn((slots, 200, HQ + 2, D), generator=g).to(torch.bfloat16).to(dev)
+        self.dev = dev
+
+    def round(self, c, ell, n_acc, spoil=None):
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=self.dev)
+        length = c.length.tolist()
+        c.reserve(i32(ell), GAMMA)
+        assert c.ell.tolist() == ell
+        x = torch.stack([self.x[r, n:n + GAMMA + 1] for r, n in enumerate(length)]).view(-1, HQ + 2, D).clone()
+        if spoil is not None:
+            x[spoil] = float("nan")
+        for layer in range(c.pool.shape[0]):
+            c.attend(layer, c.append(layer, x[:, :HQ], x[:, HQ:HQ + 1], x[:, HQ + 1:]))
+        before = c.mass.clone()
+        c.commit(i32(n_acc))
+        torch.cuda.synchronize()
+        return before
+
+
+@pytest.mark.parametrize("fade,window", [(1.0, 0), (0.75, 0), (1.0, 20)])
+def test_a_rejected_page_leaves_no_mass(fade, window, dev):
+    """Pages of rejected drafts go with the commit, and their mass with them: what
+    is written there later starts from nothing."""
+    from semi_ar_draft_round_amd.cache import PagedCache
+    say(f"[mass] rejected {fade} {window}")
+    c, rows = PagedCache(2, 2, 150, 30, 1, D, page=P, budget=50, fade=fade, window=window), Rows(dev, 2, 1)
+    for _ in range(2):
+        rows.round(c, [14, 20], [14, 20])
+    before = rows.round(c, [20, 20], [1, 0])         # tokens 30 .. 50 and 42 .. 62: 32 and 43 stay
+    assert c.length.tolist() == [32, 43]
+    assert (before[0, 2:4] > 0).all() and before[1, 3] > 0
+    assert not c.mass[0, 2:].any() and not c.mass[1, 3:].any()
+    if window:
+        assert (c.table[1, 0] < 0) and c.mass[1, 0] == 0
+    # the next round's pages start from nothing: no more than the rows' shares
+    m = c.mass.clone()
+    rows.round(c, [0, 10], [0, 10])
+    assert c.length.tolist() == [33, 54]
+    gained = (c.mass - m * fade).sum(dim=1)
+    want = torch.tensor([1.0, 11.0], device=dev) * HQ * 2
+    got = gained if not window else gained[:1]
+    # every row and head shares out one a layer; a window's release takes its page's share along
+    assert bool(((got - want[:len(got)]).abs() < 1e-3 * want[:len(got)]).all()), gained
+    assert 0 < float(c.mass[0, 2]) <= HQ * 2 * 1.001
