@@ -215,13 +215,14 @@ dspark_status dspark_cache_read(int fmt, int R, int T, int Hkv, int D, int P, in
  * Scores and sums are fp32, the sum in an order that follows from the batch
  * (the same call gives the same bits).  What an invisible token holds has no
  * effect; a row that sees nothing (lse -inf) adds nothing; a NaN among the
- * visible keys, in q or in lse makes the page's mass NaN.
+ * visible keys, in q or in lse makes the page's mass NaN, which it stays until
+ * a call with keep = 0: that takes the old mass for 0 whatever it is.
  *
  *   q, scale, window, sinks, row0, ell, len, table, pool  as in
  *        dspark_cache_attention (values are not read)
  *   lse  [rows][Hq] f32, dspark_cache_attention's
  *   keep finite and >= 0
- *   mass [R][max_pages] f32 in/out
+ *   mass [R][max_pages] f32 in/out (with keep = 0 out, but for requests without rows)
  *
  * Limits: as dspark_cache_attention.
  */

@@ -271,7 +271,7 @@ __global__ __launch_bounds__(waves_of(D) * 64) void cache_weigh_kernel(WeighArgs
         for (int w = 0; w < W; ++w) m += lds_sum[w][odd * kRun + c];
         if (s < b.pages) {
           float* p = a.mass + static_cast<int64_t>(r) * a.max_pages + s;
-          *p = __builtin_fmaf(a.keep, *p, m);
+          *p = a.keep == 0.f ? m : __builtin_fmaf(a.keep, *p, m);  // (0: whatever was there)
         }
       }
       __syncthreads();
@@ -285,8 +285,10 @@ __global__ __launch_bounds__(waves_of(D) * 64) void cache_weigh_kernel(WeighArgs
       const int r = static_cast<int>(x / parts), s = static_cast<int>(x % parts) * T + threadIdx.x;
       const Span b = span_of(a, r, chunk);
       const int c = (TWO ? s >> 1 : s);
-      if (b.n > 0 && s < a.max_pages && (s >= b.pages || (c >= b.head && c < b.first)))
-        a.mass[static_cast<int64_t>(r) * a.max_pages + s] *= a.keep;
+      if (b.n > 0 && s < a.max_pages && (s >= b.pages || (c >= b.head && c < b.first))) {
+        float* p = a.mass + static_cast<int64_t>(r) * a.max_pages + s;
+        *p = a.keep == 0.f ? 0.f : a.keep * *p;
+      }
     }
   }
 }

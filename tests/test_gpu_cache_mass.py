@@ -74,3 +74,35 @@ def test_a_rejected_page_leaves_no_mass(fade, window, dev):
     # every row and head shares out one a layer; a window's release takes its page's share along
     assert bool(((got - want[:len(got)]).abs() < 1e-3 * want[:len(got)]).all()), gained
     assert 0 < float(c.mass[0, 2]) <= HQ * 2 * 1.001
+
+
+def test_a_rejected_row_that_is_not_finite(dev):
+    """A NaN among rejected rows: the mass of the pages that it alone wrote is 0
+    again, that of those it saw is NaN until it is weighed with keep = 0."""
+    from semi_ar_draft_round_amd.cache import PagedCache
+    say("[mass] NaN")
+    for fmt in (1, 4):
+        c, rows = PagedCache(1, 1, 150, 10, 1, D, page=P, fmt=fmt, budget=50, fade=0.0), Rows(dev, 1, 2)
+        rows.round(c, [19], [19])
+        before = rows.round(c, [20], [3], spoil=20)
+        assert torch.isnan(before[0, :3]).all()
+        assert torch.isnan(c.mass[0, :2]).all() and not c.mass[0, 2:].any()
+        rows.round(c, [2], [2])
+        assert torch.isfinite(c.mass).all() and abs(float(c.mass.sum()) - 3 * HQ) < 1e-3 * 3 * HQ
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_keep_0_takes_any_mass_for_0(page, dev):
+    """Entries that rows see, that lie between the first tokens and the window,
+    and behind the last row: NaN and infinities there before make no difference,
+    and requests without rows are left alone."""
+    from test_gpu_cache_weigh import Case
+    say(f"[mass] keep 0, pages of {page}")
+    c = Case(dev, 1, [700, 40, 90], [16, -1, 3], 4, 2, 64, page, 16, window=100, sinks=20, more=300, seed=3)
+    zero = torch.zeros(c.old.shape, device=dev)
+    want = c.call(0.0, zero.clone())
+    assert (want[0, 2:500 // page] == 0).all() and (want[0] > 0).any() and (want[:, -1] == 0).all()
+    for x in (float("nan"), float("inf"), -float("inf")):
+        got = c.call(0.0, torch.full_like(zero, x))
+        assert (got[[0, 2]] == want[[0, 2]]).all()
+        assert (got[1] == x).all() or (x != x and (got[1] != got[1]).all())
