@@ -140,10 +140,13 @@ class PagedCache:
                                  sinks=max(self.keep_first, self.sinks), recent=self.keep_last, freed=self.freed)
 
     def fork(self, parent):
-        """Request r takes over parent[r]'s tokens, shared (r: stays; -1: empty)."""
+        """Request r takes over parent[r]'s tokens, shared (r: stays; -1: empty),
+        and with them its budget and the weights of its pages (-1: keeps its
+        budget)."""
         B.dspark_cache_fork(self.table, self.length, self.ref, self.bits, parent, page=self.page, ws=self.ws)
         if self.mass is not None:
             self.mass.copy_(rows_of_parents(self.mass, parent, empty=True))
+            self.budget.copy_(rows_of_parents(self.budget, parent, empty=False))
 
     def compact(self):
         """Pages in use to the low ids of every layer's pool."""

@@ -106,3 +106,24 @@ def test_keep_0_takes_any_mass_for_0(page, dev):
         got = c.call(0.0, torch.full_like(zero, x))
         assert (got[[0, 2]] == want[[0, 2]]).all()
         assert (got[1] == x).all() or (x != x and (got[1] != got[1]).all())
+
+
+def test_a_fork_takes_the_budget_along(dev):
+    """Requests of different budgets change places: each is held to its own at
+    the next commit, as if it had stayed where it was."""
+    from semi_ar_draft_round_amd.cache import PagedCache
+    say("[mass] budgets")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)
+    for swap in (False, True):
+        c, rows = PagedCache(1, 4, 150, 60, 1, D, page=P, budget=2 ** 31 - 1), Rows(dev, 4, 3)
+        c.budget.copy_(i32(2, 50, -1, 3))
+        for _ in range(4):
+            rows.round(c, [20] * 4, [20] * 4)
+        assert [int((t >= 0).sum()) for t in c.table] == [2, 6, 6, 3]
+        if swap:
+            c.fork(i32(1, 0, 2, -1))
+            rows.x[[0, 1]] = rows.x[[1, 0]]
+            assert c.budget.tolist() == [50, 2, -1, 3]
+        rows.round(c, [20] * 4, [20] * 4)
+        held = [int((t >= 0).sum()) for t in c.table]
+        assert held == ([7, 2, 7, 2] if swap else [2, 7, 7, 3])
