@@ -54,6 +54,10 @@ class Conditions:
         """Slot r goes on from parent[r]'s history and conditions (r: its own;
         -1: an empty history; values outside [-1, slots) leave r alone)."""
         from .cache import rows_of_parents
+        if parent.shape != self.state.shape[:1] or parent.dtype not in (torch.int32, torch.int64) or (
+                parent.device != self.state.device):
+            raise ValueError(f"parent must be [{self.state.shape[0]}] int32 on {self.state.device}, not "
+                             f"{list(parent.shape)} {parent.dtype} on {parent.device}")
         for t in (self.state, self.repetition, self.presence, self.frequency, self.bias_tok, self.bias):
             if t is not None:
                 t.copy_(rows_of_parents(t, parent, empty=t is self.state))
