@@ -371,6 +371,8 @@ dspark_status dspark_schedule_noalloc(int R, int gamma, const float* c, const do
  * next_tok[r] is the smallest v with cumsum(res)[v] > u_res[r] * sum(res),
  * res = max(0, p_t - p_d) on row n_acc[r] after a rejection, res = p_t of
  * row ell[r] otherwise; if sum(res) <= 0 the draw uses p_t of the same row.
+ * The sums are fp32, but a token that the target rules out (-inf, where the row
+ * has a finite logit) is neither accepted nor drawn.
  *
  *   target  target logits, dt: dense [R][gamma+1][V] when row0 == NULL, else
  *           a packed [rows][V] array whose rows row0[r] .. row0[r] + ell[r]

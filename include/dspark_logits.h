@@ -7,7 +7,8 @@
  * allows.  Row i of request r follows its history, the anchor x0 and the
  * drafts x_1 .. x_i, so the rows of one round differ in what they penalise.
  * Verified against such rows, the round's tokens are distributed as if they had
- * been drawn from them one at a time (notes, lossless verification).
+ * been drawn from them one at a time (notes, lossless verification), and none is
+ * one that its row does not allow.
  *
  *   dspark_logits         the rows' logits with all of it applied
  *   dspark_logits_prompt  a slot's history: a new prompt

@@ -9,7 +9,8 @@
 // two threads a dim, whatever D is, a task has 16 slots of D / 8 threads:
 //   keys     a slot for a (head, row): as many heads as have room, so that the
 //            few rows that most requests bring fill the work group; fp64, so
-//            that a code does not depend on the order of a sum;
+//            that a code does not depend on the order of a sum (but in the last
+//            bit of its sines, which are made by turning on from a run's first);
 //   values   a thread for a dim's 8 tokens, a word of the pages: one head, or
 //            two where the rows touch one half of the block;
 //   queries  a slot for a (row, head).
@@ -22,9 +23,10 @@
 // codes are loads one after another, and a block's bounds need all of its rows.
 // With 8 heads of keys of 128 dims: one token, 32 query heads, 4.5 .. 5.1 us;
 // 128 requests of up to 17 packed rows, 56 query heads, 22 .. 24 us, 31 MB, and
-// 31 with the read of their page tables after them.  Those took 40 with a wave
-// for a head and all its rows, in fp64 also where there are none, and 43 with
-// contiguous runs of tasks instead of every y-th.
+// 31 with the read of their page tables after them, where the 16-bit append of
+// the same rows takes 12.3.  Those took 40 with a wave for a head and all its
+// rows, in fp64 also where there are none, and 43 with contiguous runs of tasks
+// instead of every y-th.
 #include "cache_rows.hpp"
 
 namespace dspark {

@@ -17,10 +17,10 @@
 // tiles of its own (rows of one row tile; 4 bits; 8 bits up to 128 dims), and
 // past the registers into a ring in LDS where several waves multiply the same
 // 16-bit tile, and for 8-bit heads of 256 dims, whose one wave a SIMD has no
-// registers to load ahead (32 single tokens over 8192 165 us straight, 101 so;
-// 16 x 17 rows 185 and 119).  8-bit tiles of shorter heads in the ring measured
-// no gain (the ragged 128 requests 607 and 606 us, 32 x 17 rows over 4096 93 and
-// 84).
+// registers to load ahead (32 single tokens over 2048 .. 8192 165 us straight, 101
+// so; 16 x 17 rows 185 and 119).  8-bit tiles of shorter heads in the ring
+// measured no gain (the ragged 128 requests 607 and 606 us, 32 x 17 rows over
+// 1024 .. 4096 93 and 84).
 //
 // Work is split over tokens as well as rows.  The units (request, row block,
 // head, tile) are numbered in that order, and every work group takes a
@@ -38,8 +38,11 @@
 // tokens 505 us) are bound by the order inside a wave: vector instructions
 // take 47 % of the issue slots and products 33 % of the matrix units' time,
 // and with two waves a SIMD neither hides the other whole; of 8 bits the same
-// requests take 607 us (4.3 TB/s; 47 % and 36 %), 32 single tokens over 16384
-// tokens 137 us, 5.0 TB/s.  Heads of 256 dims have one wave a SIMD, where
+// requests take 604 .. 629 us (4.2 TB/s; 47 % and 36 %), 32 single tokens over
+// 4096 .. 16384 tokens 137 us, 5.0 TB/s.  A page that the table does not have
+// costs what one that it has does: its tiles are page 0's, masked (32 single
+// tokens over 131072 with 48 of 2048 pages left 1296 us of 8 bits, over those 48
+// pages alone 42).  Heads of 256 dims have one wave a SIMD, where
 // nothing but the wave itself does; 65 .. 96 query rows are three row tiles, and
 // the fourth wave of the work group idles.
 // Short contexts are bound by the two launches and the chain of loads before

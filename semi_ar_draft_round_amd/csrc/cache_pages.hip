@@ -1,5 +1,4 @@
-// Who owns the cache's pages: reserve, commit, evict, fork, compact, copy,
-// reset
+// Who owns the cache's pages: reserve, commit, evict, fork, compact, copy, reset
 // (include/dspark_cache.h).
 //
 // The free pages are a bitmap, so that which ids come next depends on the set
@@ -604,8 +603,9 @@ hipError_t cache_evict_launch(int R, int P, int n_pages, int max_pages, int sink
     kernel<<<R, threads, 0, s>>>(P, n_pages, max_pages, sinks, recent, budget, len, mass, table, ref, bits, freed);
   };
   // few entries: a small work group, whose barriers cost less.  A request of 128
-  // pages takes 5.1 us (1024 threads 5.9), 64 of 256 8.6 (9.1), of 512 9.5 (9.8),
-  // of 768 11.9 (10.9).  Long tables are read again in each pass: 64 of up to
+  // pages takes 5.1 us (1024 threads 5.9), of 256 5.9 (6.2), 64 of 256 8.6 (9.1), of
+  // 512 9.5 (9.8), 256 of 512 11.6 (11.9); but a lone one of 400 pages 7.6 (6.9 ..
+  // 7.1), of 512 7.0 (6.9), and 64 of 768 would take 11.9 (10.9).  Long tables are read again in each pass: 64 of up to
   // 8192 would take 38 so, 30 with their keys in registers.
   if (max_pages <= 4 * 128) launch(cache_evict_kernel<128, false>, 128);
   else if (max_pages <= kEvictPer * kT) launch(cache_evict_kernel<kT, false>, kT);

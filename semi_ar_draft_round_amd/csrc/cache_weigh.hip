@@ -18,7 +18,9 @@
 // ragged contexts up to 8192 take 247 us with 16-bit pages of 8 heads of 128
 // dims, 5.3 TB/s of the 1.30 GB of keys (277 in a graph, one after another; 1.44
 // GB fetched; vector units busy 28 % of the time, matrix units 15); 32 single
-// tokens over 16384 tokens of 8 bits 79 us.  A short context is a chain of loads
+// tokens over 4096 .. 16384 tokens of 8 bits 79 us.  Chunks of missing pages are
+// loaded too, not multiplied (32 single tokens over 131072 tokens with 48 of 2048
+// pages left 276 us, over those 48 pages alone 38).  A short context is a chain of loads
 // (lengths, page ids, query rows, keys) and barriers: one token over 4095 tokens
 // 9.1 us.  With work groups of four waves the ragged requests took 292 in a
 // graph, the one token 2.1 us more, chunks of 512 rows 366 us instead of 191;
