@@ -125,3 +125,46 @@ def test_rows_that_allow_one_token_or_none(V, dtype, dev):
         assert np.all(draw(dev, row, u) == only)
     tok = draw(dev, torch.full((V,), -float("inf")).to(dtype), u)
     assert np.all((tok >= 0) & (tok < V))
+
+
+@pytest.mark.parametrize("w", [dict(R=130, gamma=4, V=4096, r=256, d=128), dict(R=70, gamma=6, V=4100, r=64, d=128),
+                               dict(R=20, gamma=5, V=1000, r=32, d=64), dict(R=40, gamma=7, V=336, r=20, d=36, dtype="f32")],
+                         ids=lambda w: f"V{w['V']}")
+def test_masked_rounds_against_oracle(w, dev):
+    """Drafts some of which a mask rules out, accepted and drawn as the oracle
+    does, from rows that dspark_logits has masked; greedily too."""
+    from oracle import verify as OV
+    from oracle.common import as_f64
+    from parity import check_verify
+    from semi_ar_draft_round_amd import binding as B
+    from semi_ar_draft_round_amd import device_round as DR
+    from semi_ar_draft_round_amd import workloads as W
+    say(f"[verify] masked rounds {w}")
+    rng = np.random.default_rng(w["V"])
+    inp = W.make_inputs(W.custom("masked", seed=71, **w))
+    d = DR.to_device(inp, dev)
+    DR.sample_conf(d)
+    d.ell.copy_(torch.from_numpy(rng.integers(0, w["gamma"] + 1, w["R"]).astype(np.int32)))
+    x = d.x.cpu().numpy()
+    R, g1, V = d.target.shape
+    allowed = rng.random((R, g1, V)) < rng.choice([0.03, 0.5, 0.9], (R, g1, 1))
+    r, i = np.mgrid[:R, :g1 - 1]
+    allowed[r, i, x] = rng.random((R, g1 - 1)) < 0.8
+    allowed[..., V - 1] = True
+    bits = np.zeros((R * g1, -(-V // 32) * 32), bool)
+    bits[:, :V] = allowed.reshape(R * g1, V)
+    mask = torch.from_numpy(np.packbits(bits, axis=1, bitorder="little").view(np.int32)).to(dev)
+    B.dspark_logits(d.target, None, d.ell, w["gamma"], None, mask=mask, out=d.target)
+    DR.verify(d)
+    DR.verify_greedy(d)
+    out = DR.outputs_to_host(d)
+    # -1e4: no mass either, and finite for the bounds
+    target = np.where(allowed, as_f64(inp.target, inp.w.dtype), -1e4)
+    rep = check_verify(inp, dict(out, ell=d.ell.cpu().numpy()), np.arange(R), target=target)
+    n, tok = out["n_acc"], out["next_tok"]
+    assert all(allowed[q, k, x[q, k]] for q in range(R) for k in range(n[q])) and allowed[np.arange(R), n, tok].all()
+    assert n.max() >= 2
+    want = OV.verify_greedy(target, None, x, d.ell.cpu().numpy())
+    assert np.array_equal(want["n_acc"], d.n_acc_g.cpu().numpy())
+    assert np.array_equal(want["next_tok"], d.next_tok_g.cpu().numpy())
+    say(f"  {rep}, up to {n.max()} accepted")
